@@ -2,6 +2,7 @@
 // argument validation, the per-device workspace, TMA tensor maps and the launch
 // sequence of the pruned-MLP block of "Representation Shift: Unifying Token
 // Compression with FlashAttention" (§3.3 Eq. (6), §3.2 Eq. (4), §3.1 pruning).
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -461,6 +462,38 @@ int check_attn_args(const void* x, int B, int L, int C, int heads, const void* W
 }
 
 }  // namespace
+
+namespace rs {
+
+int device_sms(int* num_sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return RS_ERR_CUDA;
+  }
+  static std::atomic<int> sms[kMaxDevices];
+  int n = sms[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      cudaGetLastError();
+      return RS_ERR_CUDA;
+    }
+    sms[dev].store(n, std::memory_order_relaxed);
+  }
+  *num_sms = n;
+  return RS_OK;
+}
+
+int device_flag(int* num_sms, int** err) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  DevState* st = nullptr;
+  RS_TRY(dev_state(&st));
+  *num_sms = st->num_sms;
+  *err = st->err;
+  return RS_OK;
+}
+
+}  // namespace rs
 
 extern "C" {
 

@@ -1,0 +1,622 @@
+// rs_fp8_gemm.cu -- the product of two operands held in 8-bit blocks (rs_fp8.cuh),
+//
+//   D[m, n] = sum_j 2^(ea[m, j] + eb[n, j]) sum_{k in block j} qa[m, k] qb[n, k],
+//
+// then out = act(D + bias) + resid, stored as bf16, fp32 or again as 8-bit blocks along n.
+//
+// tcgen05 kind::mxf8f6f4: the E8M0 scales multiply inside the matrix instruction, so the fp32
+// accumulator stays in TMEM over the whole reduction. The instruction takes a scale per 32 K
+// elements; a block of 128 names the same byte four times. Scale tiles (128 rows x 4 blocks,
+// 512 bytes) come with every fourth K block by TMA and go to TMEM by tcgen05.cp, ordered
+// before the MMAs that read them; two sets of TMEM columns take turns.
+//
+// One persistent CTA per SM (or a CTA pair with 256-row tiles) loops over 128 x BN tiles:
+//   warps 0-7  epilogue: a tile's accumulator goes to registers at once (up to 128 columns a
+//              thread) and is handed back, then bias, activation, residual and rounding, and
+//              out through per-warp TMA-store boxes
+//   warp 8     TMA producer, warp 9 TMEM owner and MMA issuer
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "rs_fp8.cuh"
+#include "rs_gelu.cuh"
+#include "rs_internal.h"
+#include "rs_ptx.cuh"
+
+namespace rs {
+
+namespace {
+
+constexpr int kGM = 128;                       // rows of A per CTA and tile
+constexpr int kGK = 128;                       // K elements (bytes) per stage
+constexpr int kGABytes = kGM * kGK;            // 16 KB
+constexpr int kGEpiWarps = 8;
+constexpr int kGThreads = (kGEpiWarps + 2) * 32;
+constexpr int kGSmemLimit = 232448;
+constexpr int kGCtrl = 512;
+constexpr int kGBoxBytes = 32 * 64;            // 32 rows of 64 bytes, 64-byte swizzle
+constexpr int kGBoxes = 2;                     // per warp
+
+__host__ __device__ constexpr int g_scale_tiles_b(int bn) { return bn > 128 ? 2 : 1; }
+__host__ __device__ constexpr int g_stage_bytes(int bn, bool pair) {
+  return kGABytes + (pair ? bn / 2 : bn) * kGK + (1 + g_scale_tiles_b(bn)) * kScaleTile;
+}
+__host__ __device__ constexpr int g_fixed(int) {
+  return 1024 + kGCtrl + kGEpiWarps * kGBoxes * kGBoxBytes;
+}
+__host__ __device__ constexpr int g_stages(int bn, bool pair) {
+  return (kGSmemLimit - g_fixed(bn)) / g_stage_bytes(bn, pair) > 8
+             ? 8
+             : (kGSmemLimit - g_fixed(bn)) / g_stage_bytes(bn, pair);
+}
+__host__ __device__ constexpr size_t g_smem(int bn, bool pair) {
+  return static_cast<size_t>(g_fixed(bn)) + g_stages(bn, pair) * g_stage_bytes(bn, pair);
+}
+
+}  // namespace
+
+template <int BN, bool PAIR, int OUT>
+__global__ void __launch_bounds__(kGThreads, 1)
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmSA,
+                    const __grid_constant__ CUtensorMap tmSB,
+                    const __grid_constant__ CUtensorMap tmOut, const Fp8Gemm p) {
+  constexpr int kBRows = PAIR ? BN / 2 : BN;
+  constexpr int kBBytes = kBRows * kGK;
+  constexpr int kSTiles = g_scale_tiles_b(BN);
+  constexpr int kSBytes = (1 + kSTiles) * kScaleTile;
+  constexpr int STAGES = g_stages(BN, PAIR);
+  constexpr int kTileM = PAIR ? 2 * kGM : kGM;
+  constexpr uint32_t kIdesc = idesc_mx_e4m3(kTileM, BN);
+  constexpr uint32_t kTx = (PAIR ? 2 : 1) * (kGABytes + kBBytes);
+  constexpr uint32_t kTxScales = (PAIR ? 2 : 1) * kSBytes;
+  constexpr int NACC = 2 * BN + 32 <= 512 ? 2 : 1;  // accumulators that fit beside the scales
+  constexpr uint32_t kScaleCol = NACC * BN;         // two sets of 4 (A) + 8 (B) columns
+  constexpr int kCols = BN / 2;                     // columns of one epilogue warp
+  static_assert(STAGES >= 3, "pipeline depth");
+  static_assert(OUT != kOutQ8 || kCols == kQBlock, "one block per epilogue thread");
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + STAGES * kGABytes;
+  uint8_t* sBox = sB + STAGES * kBBytes;
+  uint8_t* sS = sBox + kGEpiWarps * kGBoxes * kGBoxBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sS + STAGES * kSBytes);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int KB = (p.K + kGK - 1) / kGK;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
+  const int unit0 = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
+  const int units = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], PAIR ? 2 * kGEpiWarps : kGEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmSA);
+    tma_prefetch_desc(&tmSB);
+    if (!p.direct) tma_prefetch_desc(&tmOut);
+  }
+  if (warp == 9) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(tmem_slot, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, 512);
+      tmem_relinquish();
+    }
+  }
+  pdl_trigger();
+  pdl_wait();
+  tc_fence_before_sync();
+  if constexpr (PAIR) {
+    cluster_sync();
+  } else {
+    __syncthreads();
+  }
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  const WaitCtl wc{abort_flag, p.err, p.timeout_ns};
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t pend_mask = 0, pend_phase = 0;
+      const uint32_t full_leader = PAIR ? mapa_shared(smem_u32(&full[0]), 0u) : 0u;
+      for (int tile = unit0; tile < p.num_tiles; tile += units) {
+        const int m_blk = tile / p.n_blocks, n_blk = tile % p.n_blocks;
+        const int a_row = m_blk * kTileM + static_cast<int>(rank) * kGM;
+        const int n0 = n_blk * BN;
+        const int b_row = n0 + static_cast<int>(rank) * kBRows;
+        bool ok = true;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!wait_bounded(&empty[stage], phase ^ 1u, wc)) { ok = false; break; }
+          const bool scales = (kb & 3) == 0;
+          if (leader) mbar_arrive_expect_tx(&full[stage], scales ? kTx + kTxScales : kTx);
+          uint8_t* dA = sA + stage * kGABytes;
+          uint8_t* dB = sB + stage * kBBytes;
+          uint8_t* dS = sS + stage * kSBytes;
+          // the A scales of this CTA's rows; B's of every column of the tile (both CTAs of a
+          // pair need them all). Tiles past the operand's rows read as zero.
+          if constexpr (PAIR) {
+            const uint32_t fb = full_leader + static_cast<uint32_t>(stage) * 8u;
+            tma_load_2d_pair(dA, &tmA, fb, kb * kGK, a_row);
+            tma_load_2d_pair(dB, &tmB, fb, kb * kGK, b_row);
+            if (scales) {
+              tma_load_3d_pair(dS, &tmSA, fb, 0, kb >> 2, a_row >> 7);
+              tma_load_3d_pair(dS + kScaleTile, &tmSB, fb, 0, kb >> 2, n0 >> 7);
+            }
+          } else {
+            tma_load_2d(dA, &tmA, &full[stage], kb * kGK, a_row);
+            tma_load_2d(dB, &tmB, &full[stage], kb * kGK, b_row);
+            if (scales) {
+              tma_load_3d(dS, &tmSA, &full[stage], 0, kb >> 2, a_row >> 7);
+              tma_load_3d(dS + kScaleTile, &tmSB, &full[stage], 0, kb >> 2, n0 >> 7);
+            }
+          }
+          const uint32_t bit = 1u << stage;
+          pend_mask |= bit;
+          pend_phase = (pend_phase & ~bit) | (phase << stage);
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+      }
+      // every copy must land before the CTA may exit (a pair's land on the leader's barriers)
+      if (leader) {
+#pragma unroll
+        for (int s = 0; s < STAGES; ++s)
+          if (pend_mask & (1u << s)) wait_bounded(&full[s], (pend_phase >> s) & 1u, wc, false);
+      }
+      if constexpr (PAIR) {
+        // and the leader's releases of every stage must have arrived here
+        for (int i = 0; i < STAGES; ++i) {
+          if (!wait_bounded(&empty[stage], phase ^ 1u, wc)) break;
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0 && leader) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      uint32_t set = 0;  // scale columns in use
+      bool issued = false;
+      for (int tile = unit0; tile < p.num_tiles; tile += units) {
+        const int n0 = (tile % p.n_blocks) * BN;
+        if (!wait_bounded(&tempty[acc], acc_phase ^ 1u, wc, true, PAIR)) break;
+        tc_fence_after_sync();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+        uint32_t ts = 0;
+        bool ok = true;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!wait_bounded(&full[stage], phase, wc)) { ok = false; break; }
+          tc_fence_after_sync();
+          if ((kb & 3) == 0) {
+            ts = tmem_base + kScaleCol + set * 16u;
+            set ^= 1u;
+            const uint64_t sd = scale_tile_desc(smem_u32(sS + stage * kSBytes));
+#pragma unroll
+            for (int i = 0; i < 1 + kSTiles; ++i) {
+              if constexpr (PAIR)
+                tmem_cp_scales_pair(ts + 4u * i, sd + static_cast<uint64_t>(i * (kScaleTile >> 4)));
+              else
+                tmem_cp_scales(ts + 4u * i, sd + static_cast<uint64_t>(i * (kScaleTile >> 4)));
+            }
+          }
+          // B's columns start inside a scale tile when BN is no multiple of 128: 32 rows a column
+          const uint32_t tsb = ts + 4u + static_cast<uint32_t>((n0 & 127) >> 5);
+          const uint32_t id = idesc_mx_byte(kIdesc, static_cast<uint32_t>(kb & 3));
+          const uint64_t ad = sw128_kmajor_desc(smem_u32(sA + stage * kGABytes));
+          const uint64_t bd = sw128_kmajor_desc(smem_u32(sB + stage * kBBytes));
+#pragma unroll
+          for (int k = 0; k < kGK / 32; ++k) {
+            // whole 32-wide steps past K hold zeros: left out
+            if (k > 0 && kb * kGK + k * 32 >= p.K) break;
+            if constexpr (PAIR)
+              umma_mx_pair(d_tmem, ad + 2u * k, bd + 2u * k, id, ts, tsb, (kb | k) != 0 ? 1u : 0u);
+            else
+              umma_mx(d_tmem, ad + 2u * k, bd + 2u * k, id, ts, tsb, (kb | k) != 0 ? 1u : 0u);
+          }
+          issued = true;
+          if constexpr (PAIR)
+            umma_commit_pair_mc(&empty[stage], 0x3);
+          else
+            umma_commit(&empty[stage]);
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        if constexpr (PAIR)
+          umma_commit_pair_mc(&tfull[acc], 0x3);
+        else
+          umma_commit(&tfull[acc]);
+        if (++acc == NACC) { acc = 0; acc_phase ^= 1u; }
+      }
+      if (*abort_flag && issued) {
+        if constexpr (PAIR)
+          umma_commit_pair(drain);
+        else
+          umma_commit(drain);
+        wait_bounded(drain, 0u, wc, false);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3, grp = warp >> 2;
+    uint8_t* box = sBox + warp * kGBoxes * kGBoxBytes;
+    constexpr int ES = OUT == kOutQ8 ? 1 : OUT == kOutBf16 ? 2 : 4;  // bytes of an output element
+    constexpr int BC = 64 / ES;                                      // columns of a box
+    constexpr int NB = kCols / BC;                                   // boxes of a tile
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    int slot = 0;
+    for (int tile = unit0; tile < p.num_tiles; tile += units) {
+      const int m_blk = tile / p.n_blocks, n_blk = tile % p.n_blocks;
+      const int row0 = m_blk * kTileM + static_cast<int>(rank) * kGM + q * 32;
+      const int col0 = n_blk * BN + grp * kCols;
+      int ok = 1;
+      if (lane == 0) ok = wait_bounded(&tfull[acc], acc_phase, wc) ? 1 : 0;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      mbar_try_wait(&tfull[acc], acc_phase);  // completed: acquire for every lane
+      tc_fence_after_sync();
+      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                             static_cast<uint32_t>(acc * BN + grp * kCols);
+      uint32_t r[kCols / 32][32];
+#pragma unroll
+      for (int i = 0; i < kCols / 32; ++i) tmem_ld32_async(t_row + 32u * i, r[i]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < kCols / 32; ++i) reg_fence(r[i]);
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR && !leader)
+          mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0u));
+        else
+          mbar_arrive(&tempty[acc]);
+      }
+      if (++acc == NACC) { acc = 0; acc_phase ^= 1u; }
+      const int row = row0 + lane;
+      const bool live = row0 < p.M && col0 < p.N;  // the warp holds part of the output
+      if (!live) continue;
+
+      // bias and activation, 32 columns at a time
+#pragma unroll
+      for (int i = 0; i < kCols / 32; ++i) {
+        const int c = col0 + 32 * i;
+        if (p.bias != nullptr) {
+          if (c + 32 <= p.N) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const uint4 b4 = __ldg(reinterpret_cast<const uint4*>(p.bias + c) + v);
+              const uint32_t bw[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float& a = reinterpret_cast<float&>(r[i][8 * v + 2 * e]);
+                float& b = reinterpret_cast<float&>(r[i][8 * v + 2 * e + 1]);
+                a += bf16lo(bw[e]);
+                b += bf16hi(bw[e]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c + e < p.N)
+                r[i][e] = __float_as_uint(__uint_as_float(r[i][e]) + __bfloat162float(p.bias[c + e]));
+          }
+        }
+        if (p.gelu) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint64_t z2[8], g2[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              z2[e] = (static_cast<uint64_t>(r[i][16 * h + 2 * e + 1]) << 32) | r[i][16 * h + 2 * e];
+            gelu2_block<8>(z2, g2);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              r[i][16 * h + 2 * e] = static_cast<uint32_t>(g2[e]);
+              r[i][16 * h + 2 * e + 1] = static_cast<uint32_t>(g2[e] >> 32);
+            }
+          }
+        }
+      }
+
+      float inv = 0.f;
+      if constexpr (OUT == kOutQ8) {
+        // this thread's 128 columns of the row are one block; columns past N hold no value
+        if (col0 + kCols > p.N) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (col0 + 32 * i + e >= p.N) r[i][e] = 0;
+        }
+        uint32_t a = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) a = max(a, r[i][e] & 0x7FFFFFFFu);
+        if (a >= kInfBits) {
+          a = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float f = __uint_as_float(r[i][e]);
+              a = max(a, finite_abs_bits(f));
+              r[i][e] = __float_as_uint(inf_to_nan(f));
+            }
+        }
+        const uint32_t byte = e8m0_byte(a);
+        inv = e8m0_inverse(byte);
+        if (row < p.M) p.out_scales[scale_offset(row, col0 >> 7, p.kqo)] = static_cast<uint8_t>(byte);
+      }
+
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int c = col0 + b * BC;
+        if (c >= p.N) break;
+        uint8_t* bx = box + slot * kGBoxBytes;
+        const uint32_t bx_u32 = smem_u32(bx);
+        uint32_t w[16];  // the row's 64 bytes
+        if constexpr (OUT == kOutQ8) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int k = b * 64 + 4 * e;
+            w[e] = e4m3x4(__uint_as_float(r[k / 32][k % 32]) * inv,
+                          __uint_as_float(r[k / 32][k % 32 + 1]) * inv,
+                          __uint_as_float(r[k / 32][k % 32 + 2]) * inv,
+                          __uint_as_float(r[k / 32][k % 32 + 3]) * inv);
+          }
+        } else {
+          float f[BC];
+#pragma unroll
+          for (int e = 0; e < BC; ++e) {
+            const int k = b * BC + e;
+            f[e] = __uint_as_float(r[k / 32][k % 32]);
+          }
+          if (p.resid != nullptr && row < p.M) {
+            const uint8_t* rr = static_cast<const uint8_t*>(p.resid) +
+                                (static_cast<int64_t>(row) * p.ldr + c) * ES;
+            if (p.rvec && c + BC <= p.N) {
+#pragma unroll
+              for (int v = 0; v < 4; ++v) {
+                const uint4 x4 = *(reinterpret_cast<const uint4*>(rr) + v);
+                const uint32_t xw[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if constexpr (OUT == kOutBf16) {
+                    f[8 * v + 2 * e] += bf16lo(xw[e]);
+                    f[8 * v + 2 * e + 1] += bf16hi(xw[e]);
+                  } else {
+                    f[4 * v + e] += __uint_as_float(xw[e]);
+                  }
+                }
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < BC; ++e)
+                if (c + e < p.N) {
+                  if constexpr (OUT == kOutBf16)
+                    f[e] += __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(rr)[e]);
+                  else
+                    f[e] += reinterpret_cast<const float*>(rr)[e];
+                }
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            if constexpr (OUT == kOutBf16)
+              w[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+            else
+              w[e] = __float_as_uint(f[e]);
+          }
+        }
+        // the store that last used this box has read it
+        if (lane == 0) bulk_wait_group_read<kGBoxes - 1>();
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          sts128(bx_u32 + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4),
+                 make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]));
+        // TMA stores whole 16-byte units: where the last columns end inside one, they and rows
+        // that TMA cannot address (a pitch or base off 16 bytes) go by plain stores,
+        // neighbouring lanes writing neighbouring elements
+        if (!p.direct && (c + BC <= p.N || OUT == kOutQ8 || p.N * ES % 16 == 0)) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tmOut, bx, c, row0);
+            bulk_commit_group();
+          }
+        } else {
+          __syncwarp();
+#pragma unroll 4
+          for (int it = 0; it < BC; ++it) {
+            const int idx = it * 32 + lane, rr = idx / BC, cc = idx % BC;
+            const uint8_t* src = bx + rr * 64 + ((((cc * ES) >> 4) ^ ((rr >> 1) & 3)) << 4) + ((cc * ES) & 15);
+            if (row0 + rr < p.M && c + cc < p.N) {
+              uint8_t* dst = static_cast<uint8_t*>(p.out) +
+                             (static_cast<int64_t>(row0 + rr) * p.ldo + c + cc) * ES;
+              if constexpr (ES == 2)
+                *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(src);
+              else if constexpr (ES == 4)
+                *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(src);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) bulk_commit_group();  // an empty group keeps the boxes' turns
+        }
+        slot ^= 1;
+      }
+    }
+    if (lane == 0) bulk_wait_group0();
+    __syncwarp();
+  }
+
+  __syncthreads();
+  if constexpr (PAIR) {
+    // as in the bf16 GEMM: after an abort, time for the other CTA's loads to land; neither CTA
+    // leaves or frees TMEM before the other is done
+    if (threadIdx.x == 0 && (*abort_flag || *reinterpret_cast<volatile int*>(p.err) != 0))
+      spin_ns(1000000);
+    cluster_sync();
+  }
+  if (warp == 9) {
+    tc_fence_after_sync();
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem_base, 512);
+    else
+      tmem_dealloc(tmem_base, 512);
+  }
+}
+
+// ------------------------------------------------------------------ host
+namespace {
+
+int tmap_2d(CUtensorMap* m, CUtensorMapDataType t, int es, const void* base, uint64_t inner,
+            uint64_t rows, uint64_t pitch, uint32_t box_inner, uint32_t box_rows,
+            CUtensorMapSwizzle sw) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return RS_ERR_CUDA;
+  cuuint64_t dims[2] = {inner, rows};
+  cuuint64_t strides[1] = {pitch * es};
+  cuuint32_t box[2] = {box_inner, box_rows};
+  cuuint32_t one[2] = {1, 1};
+  return fn(m, t, 2, const_cast<void*>(base), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? RS_OK
+             : RS_ERR_CUDA;
+}
+
+// Scale tiles as [row tiles][tiles along K][128 words].
+int tmap_scales(CUtensorMap* m, const void* base, int rows, int K, uint32_t tiles) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return RS_ERR_CUDA;
+  const cuuint64_t kq = (K + 511) / 512, rt = (rows + 127) / 128;
+  cuuint64_t dims[3] = {128, kq, rt};
+  cuuint64_t strides[2] = {kScaleTile, kScaleTile * kq};
+  cuuint32_t box[3] = {128, 1, tiles};
+  cuuint32_t one[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? RS_OK
+             : RS_ERR_CUDA;
+}
+
+template <int BN, bool PAIR, int OUT>
+int go(Fp8Gemm p, int num_sms, cudaStream_t s, bool pdl) {
+  constexpr int tile_m = PAIR ? 256 : 128;
+  p.n_blocks = (p.N + BN - 1) / BN;
+  p.num_tiles = ((p.M + tile_m - 1) / tile_m) * p.n_blocks;
+  CUtensorMap tA, tB, tSA, tSB, tO{};
+  const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  int st = tmap_2d(&tA, u8, 1, p.a, p.K, p.M, p.lda, kGK, kGM, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st == RS_OK)
+    st = tmap_2d(&tB, u8, 1, p.b, p.K, p.N, p.ldb, kGK, PAIR ? BN / 2 : BN,
+                 CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st == RS_OK) st = tmap_scales(&tSA, p.sa, p.M, p.K, 1);
+  if (st == RS_OK) st = tmap_scales(&tSB, p.sb, p.N, p.K, g_scale_tiles_b(BN));
+  constexpr int es = OUT == kOutQ8 ? 1 : OUT == kOutBf16 ? 2 : 4;
+  if (st == RS_OK && !p.direct)
+    st = tmap_2d(&tO, OUT == kOutQ8     ? u8
+                      : OUT == kOutBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                 es, p.out, p.N, p.M, p.ldo, 64 / es, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (st != RS_OK) return st;
+  auto kern = fp8_gemm_kernel<BN, PAIR, OUT>;
+  constexpr size_t smem = g_smem(BN, PAIR);
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess) {
+    cudaGetLastError();
+    return RS_ERR_CUDA;
+  }
+  cudaError_t e;
+  if constexpr (PAIR) {
+    static const int max_pairs = [&]() {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(2 * (num_sms / 2));
+      cfg.blockDim = dim3(kGThreads);
+      cfg.dynamicSmemBytes = smem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        n = num_sms / 2;
+      }
+      return n < num_sms / 2 ? n : num_sms / 2;
+    }();
+    const int pairs = p.num_tiles < max_pairs ? p.num_tiles : max_pairs;
+    e = launch_cluster(kern, dim3(2 * pairs), dim3(kGThreads), smem, s, pdl, 2, tA, tB, tSA, tSB, tO,
+                       p);
+  } else {
+    const int grid = p.num_tiles < num_sms ? p.num_tiles : num_sms;
+    e = launch(kern, dim3(grid), dim3(kGThreads), smem, s, pdl, tA, tB, tSA, tSB, tO, p);
+  }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return RS_ERR_CUDA;
+  }
+  return RS_OK;
+}
+
+template <int OUT>
+int pick(const Fp8Gemm& p, int num_sms, cudaStream_t s, bool pdl) {
+  const bool pair = p.M > 128;
+  if constexpr (OUT != kOutQ8) {
+    if (p.N <= 128)
+      return pair ? go<128, true, OUT>(p, num_sms, s, pdl) : go<128, false, OUT>(p, num_sms, s, pdl);
+  }
+  return pair ? go<256, true, OUT>(p, num_sms, s, pdl) : go<256, false, OUT>(p, num_sms, s, pdl);
+}
+
+}  // namespace
+
+int launch_fp8_gemm(const Fp8Gemm& p, int out, int num_sms, cudaStream_t s, bool pdl) {
+  switch (out) {
+    case kOutBf16: return pick<kOutBf16>(p, num_sms, s, pdl);
+    case kOutFp32: return pick<kOutFp32>(p, num_sms, s, pdl);
+    default: return pick<kOutQ8>(p, num_sms, s, pdl);
+  }
+}
+
+}  // namespace rs

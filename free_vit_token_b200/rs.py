@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -25,6 +25,7 @@ RS_ERR_DEVICE_TIMEOUT = 6
 RS_ERR_NO_MEM = 7
 
 _vp, _i, _fp, _ip = ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p
+_l, _u = ctypes.c_int64, ctypes.c_uint64
 SIGNATURES = {
     "rs_block_forward": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _ip,
                               _fp, _vp]),
@@ -59,6 +60,26 @@ SIGNATURES = {
                                 _vp, _ip, _fp, _vp]),
     "rs_mlp_fused_supported": (_i, [_i, _i]),
     "rs_mlp_fused": (_i, [_vp, _fp, _vp, _fp, _fp, _i, _i, _i, _vp, _vp, _vp, _fp, _vp]),
+    "rs_ln_forward": (_i, [_vp, _l, _i, _i, _i, _vp, _vp, _i, ctypes.c_float, _vp, _l, _fp, _vp]),
+    "rs_ln_quantize": (_i, [_vp, _l, _i, _i, _i, _vp, _vp, _i, ctypes.c_float, _vp, _l, _vp, _fp,
+                            _vp]),
+    "rs_ln_backward": (_i, [_vp, _l, _vp, _l, _vp, _l, _fp, _vp, _i, _i, _i, _i, _vp, _l, _fp, _fp,
+                            _vp, _u, _vp]),
+    "rs_ln_backward_ws_bytes": (_u, [_i, _i]),
+    "rs_fp8_scale_bytes": (_u, [_i, _i]),
+    "rs_fp8_quantize": (_i, [_vp, _l, _i, _i, _i, _vp, _l, _vp, _vp, _l, _vp, _fp, _vp, _u, _vp]),
+    "rs_fp8_quantize_ws_bytes": (_u, [_i, _i]),
+    "rs_fp8_gemm": (_i, [_vp, _l, _vp, _vp, _l, _vp, _i, _i, _i, _vp, _i, _vp, _l, _vp, _l, _i, _vp,
+                         _vp]),
+    "rs_fp8_linear": (_i, [_vp, _l, _i, _i, _i, _vp, _l, _vp, _vp, _i, _vp, _l, _vp, _l, _vp, _u,
+                           _vp]),
+    "rs_fp8_linear_ws_bytes": (_u, [_i, _i]),
+    "rs_fp8_linear_backward": (_i, [_vp, _l, _i, _i, _i, _vp, _l, _vp, _vp, _l, _vp, _vp, _l, _vp,
+                                    _l, _i, _fp, _vp, _u, _vp]),
+    "rs_fp8_linear_backward_ws_bytes": (_u, [_i, _i]),
+    "rs_mlp_forward_fp8": (_i, [_vp, _i, _i, _i, _vp, _l, _vp, _vp, _vp, _l, _vp, _vp, _vp, _vp,
+                                _vp, _vp, _u, _vp]),
+    "rs_mlp_forward_fp8_ws_bytes": (_u, [_i, _i, _i]),
     "rs_status_string": (ctypes.c_char_p, [_i]),
     "rs_get_last_device_error": (_i, [_vp]),
     "rs_release_workspace": (None, []),
@@ -470,3 +491,316 @@ def rs_debug_attn_skip_load(qkv: torch.Tensor, heads: int, out: torch.Tensor, sk
     _check(lib().rs_debug_attn_skip_load(_ptr(qkv), B, L, int(heads), _ptr(out), int(skip_block),
                                          int(timeout_us), _stream(stream)),
            "rs_debug_attn_skip_load")
+
+
+# ------------------------------------------------------------------ layer norm, 8-bit blocks
+RS_BF16, RS_FP16, RS_FP32, RS_E4M3 = 0, 1, 2, 3
+RS_MAX_LN_C = 8192
+_DTYPES = {torch.bfloat16: RS_BF16, torch.float16: RS_FP16, torch.float32: RS_FP32}
+
+
+class Fp8(NamedTuple):
+    """A matrix [rows, K] in 8-bit blocks: ``q`` [rows, ld] float8_e4m3fn (ld >= K, a
+    multiple of 16) and ``scales``, a flat uint8 tensor of rs_fp8_scale_bytes(rows, K) bytes
+    with one power of two per 128 values of a row (their order: include/rs.h)."""
+
+    q: torch.Tensor
+    scales: torch.Tensor
+    rows: int
+    K: int
+
+
+def _rows(t: torch.Tensor, name: str, width: Optional[int] = None,
+          dtype: Optional[torch.dtype] = None, rows: Optional[int] = None) -> Tuple[int, int, int]:
+    """(address, row stride, rows) of a matrix whose rows may be strided; tensors of more
+    dimensions count as their rows and must be contiguous."""
+    if t.dim() == 2:
+        n, w = t.shape
+        ld, step = t.stride()
+        if w > 1 and step != 1:
+            raise ValueError(f"{name}: the elements of a row must be contiguous")
+        if n < 2 or w == 0:
+            ld = max(ld, w, 1) if n else max(w, 1)
+    else:
+        if not t.is_contiguous() or t.dim() == 0:
+            raise ValueError(f"{name} must be a matrix or a contiguous tensor")
+        w = t.shape[-1]
+        n, ld = t.numel() // max(w, 1), w
+    if ld < w:
+        raise ValueError(f"{name}: rows overlap")
+    if width is not None and w != width:
+        raise ValueError(f"{name}: rows of {width} wanted, got {w}")
+    if rows is not None and n != rows:
+        raise ValueError(f"{name}: {rows} rows wanted, got {n}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: {dtype} wanted, got {t.dtype}")
+    _on_device(t, name)
+    return t.data_ptr() or None, ld, n
+
+
+def _on_device(t: torch.Tensor, name: str) -> None:
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+
+
+def _vec(t: Optional[torch.Tensor], name: str, n: int, dtype: torch.dtype) -> Optional[int]:
+    """Address of a contiguous vector of n elements (None for None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of {n} elements wanted")
+    _on_device(t, name)
+    return t.data_ptr() or None
+
+
+def _params(x: torch.Tensor, C: int, gamma, beta) -> Tuple[int, Optional[int], Optional[int]]:
+    dt = gamma.dtype if gamma is not None else beta.dtype if beta is not None else x.dtype
+    if dt != torch.float32 and dt != x.dtype:
+        raise ValueError("gamma and beta must be float32 or of x's type")
+    return _DTYPES[dt], _vec(gamma, "gamma", C, dt), _vec(beta, "beta", C, dt)
+
+
+def _float_type(x: torch.Tensor) -> int:
+    if x.dtype not in _DTYPES:
+        raise ValueError("bfloat16, float16 or float32 wanted")
+    return _DTYPES[x.dtype]
+
+
+def _ws(n: int, dev, ws: Optional[torch.Tensor]) -> Tuple[Optional[int], int, Optional[torch.Tensor]]:
+    """The caller's scratch tensor, or one of n bytes from torch's allocator (the tensor is
+    returned too: it must live until the call is queued)."""
+    if ws is None:
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    else:
+        if not ws.is_contiguous():
+            raise ValueError("ws must be contiguous")
+        _on_device(ws, "ws")
+    return ws.data_ptr() or None, ws.numel() * ws.element_size(), ws
+
+
+def _fp8_empty(rows: int, K: int, dev) -> Fp8:
+    q = torch.empty(rows, (K + 15) // 16 * 16, dtype=torch.float8_e4m3fn, device=dev)
+    n = (rows + 127) // 128 * ((K + 511) // 512) * 512
+    return Fp8(q, torch.empty(n, dtype=torch.uint8, device=dev), rows, K)
+
+
+def _fp8(t: Fp8, name: str, rows: Optional[int] = None, K: Optional[int] = None):
+    """(q address, row stride, scales address) of a quantised operand."""
+    if (rows is not None and t.rows != rows) or (K is not None and t.K != K):
+        raise ValueError(f"{name}: [{rows}, {K}] wanted, got [{t.rows}, {t.K}]")
+    q, ld, _ = _rows(t.q, name, dtype=torch.float8_e4m3fn, rows=t.rows)
+    if t.q.shape[-1] < t.K:
+        raise ValueError(f"{name}: rows shorter than K")
+    if t.scales.numel() < (t.rows + 127) // 128 * ((t.K + 511) // 512) * 512:
+        raise ValueError(f"{name}: too few scale bytes")
+    return q, ld, _vec(t.scales, f"{name} scales", t.scales.numel(), torch.uint8)
+
+
+def rs_ln_forward(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
+                  beta: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                  y: Optional[torch.Tensor] = None, stats: Optional[torch.Tensor] = None,
+                  stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """x [..., C] (bf16, fp16 or fp32; a matrix may have strided rows) -> (LN(x) of the same
+    type, stats [M, 2] fp32 with each row's mean and 1/std for rs_ln_backward)."""
+    dt = _float_type(x)
+    C = x.shape[-1]
+    px, ldx, M = _rows(x, "x")
+    pdt, pg, pb = _params(x, C, gamma, beta)
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if stats is None:
+        stats = torch.empty(M, 2, dtype=torch.float32, device=x.device)
+    py, ldy, _ = _rows(y, "y", C, x.dtype, M)
+    _check(lib().rs_ln_forward(px, ldx, M, C, dt, pg, pb, pdt, eps, py, ldy,
+                               _vec(stats, "stats", 2 * M, torch.float32), _stream(stream)),
+           "rs_ln_forward")
+    return y, stats
+
+
+def rs_ln_quantize(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
+                   beta: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                   out: Optional[Fp8] = None, stats: Optional[torch.Tensor] = None,
+                   stream=None) -> Fp8:
+    """LN(x) in 8-bit blocks along C (x bf16 or fp16, C a multiple of 8); `stats` [M, 2] fp32
+    also receives each row's mean and 1/std."""
+    dt = _float_type(x)
+    C = x.shape[-1]
+    px, ldx, M = _rows(x, "x")
+    pdt, pg, pb = _params(x, C, gamma, beta)
+    if out is None:
+        out = _fp8_empty(M, C, x.device)
+    q, ldq, sc = _fp8(out, "out", M, C)
+    _check(lib().rs_ln_quantize(px, ldx, M, C, dt, pg, pb, pdt, eps, q, ldq, sc,
+                                _vec(stats, "stats", 2 * M, torch.float32), _stream(stream)),
+           "rs_ln_quantize")
+    return out
+
+
+def rs_ln_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor,
+                   gamma: Optional[torch.Tensor] = None, dres: Optional[torch.Tensor] = None,
+                   dx: Optional[torch.Tensor] = None, dgamma: Optional[torch.Tensor] = None,
+                   dbeta: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                   stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Gradients of y = LN(x) for dy: (dx, of x's type, with `dres` added; dgamma [C] fp32;
+    dbeta [C] fp32). `stats` as rs_ln_forward returned them; dx may be dres."""
+    dt = _float_type(x)
+    C = x.shape[-1]
+    px, ldx, M = _rows(x, "x")
+    pdy, lddy, _ = _rows(dy, "dy", C, x.dtype, M)
+    pdr, lddr = (None, C) if dres is None else _rows(dres, "dres", C, x.dtype, M)[:2]
+    pdt, pg, _ = _params(x, C, gamma, None)
+    dev = x.device
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    if dgamma is None:
+        dgamma = torch.empty(C, dtype=torch.float32, device=dev)
+    if dbeta is None:
+        dbeta = torch.empty(C, dtype=torch.float32, device=dev)
+    pdx, lddx, _ = _rows(dx, "dx", C, x.dtype, M)
+    n = 0 if ws is not None else lib().rs_ln_backward_ws_bytes(M, C)
+    pw, nw, ws = _ws(n, dev, ws)
+    st = lib().rs_ln_backward(pdy, lddy, px, ldx, pdr, lddr,
+                              _vec(stats, "stats", 2 * M, torch.float32), pg, pdt, M, C, dt, pdx,
+                              lddx, _vec(dgamma, "dgamma", C, torch.float32),
+                              _vec(dbeta, "dbeta", C, torch.float32), pw, nw, _stream(stream))
+    _check(st, "rs_ln_backward")
+    return dx, dgamma, dbeta
+
+
+def rs_fp8_scale_bytes(rows: int, K: int) -> int:
+    return int(lib().rs_fp8_scale_bytes(int(rows), int(K)))
+
+
+def rs_fp8_quantize(x: torch.Tensor, rows: bool = True, cols: bool = False, colsum: bool = False,
+                    out: Optional[Fp8] = None, out_t: Optional[Fp8] = None, stream=None
+                    ) -> Tuple[Optional[Fp8], Optional[Fp8], Optional[torch.Tensor]]:
+    """x [M, K] (bf16, fp16 or fp32) to 8-bit blocks of 128 along K (`rows`), and/or its
+    transpose [K, M] in blocks along M (`cols`), and/or its column sums [K] fp32 (`colsum`,
+    needs cols), from one read: a triple, None for what was not asked for."""
+    dt = _float_type(x)
+    K = x.shape[-1]
+    px, ldx, M = _rows(x, "x")
+    dev = x.device
+    if colsum and not cols:
+        raise ValueError("colsum needs cols")
+    if rows and out is None:
+        out = _fp8_empty(M, K, dev)
+    if cols and out_t is None:
+        out_t = _fp8_empty(K, M, dev)
+    q, ldq, sc = _fp8(out, "out", M, K) if rows else (None, 0, None)
+    qt, ldqt, sct = _fp8(out_t, "out_t", K, M) if cols else (None, 0, None)
+    sums, ws, pw, nw = None, None, None, 0
+    if colsum:
+        sums = torch.empty(K, dtype=torch.float32, device=dev)
+        pw, nw, ws = _ws(lib().rs_fp8_quantize_ws_bytes(M, K), dev, None)
+    _check(lib().rs_fp8_quantize(px, ldx, M, K, dt, q, ldq, sc, qt, ldqt, sct,
+                                 None if sums is None else sums.data_ptr(), pw, nw,
+                                 _stream(stream)), "rs_fp8_quantize")
+    return out if rows else None, out_t if cols else None, sums
+
+
+def rs_fp8_gemm(a: Fp8, b: Fp8, bias: Optional[torch.Tensor] = None, gelu: bool = False,
+                resid: Optional[torch.Tensor] = None, out=None,
+                out_dtype: Optional[torch.dtype] = None, stream=None):
+    """act(A B^T + bias) + resid of two quantised operands [M, K] and [N, K]: a bf16 (default)
+    or fp32 tensor [M, N], or with out_dtype=torch.float8_e4m3fn an Fp8."""
+    M, N, K = a.rows, b.rows, a.K
+    pa, lda, sa = _fp8(a, "a")
+    pb, ldb, sb = _fp8(b, "b", K=K)
+    if out_dtype is None:
+        out_dtype = (torch.bfloat16 if out is None else
+                     torch.float8_e4m3fn if isinstance(out, Fp8) else out.dtype)
+    if out_dtype == torch.float8_e4m3fn:
+        if out is None:
+            out = _fp8_empty(M, N, a.q.device)
+        po, ldo, so = _fp8(out, "out", M, N)
+        dt = RS_E4M3
+    else:
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("out_dtype: bfloat16, float32 or float8_e4m3fn")
+        if out is None:
+            out = torch.empty(M, N, dtype=out_dtype, device=a.q.device)
+        po, ldo, _ = _rows(out, "out", N, out_dtype, M)
+        so, dt = None, _DTYPES[out_dtype]
+    pr, ldr = (None, N) if resid is None else _rows(resid, "resid", N, out_dtype, M)[:2]
+    _check(lib().rs_fp8_gemm(pa, lda, sa, pb, ldb, sb, M, N, K,
+                             _vec(bias, "bias", N, torch.bfloat16), int(gelu), pr, ldr, po, ldo,
+                             dt, so, _stream(stream)), "rs_fp8_gemm")
+    return out
+
+
+def rs_fp8_linear(x: torch.Tensor, w: Fp8, bias: Optional[torch.Tensor] = None,
+                  gelu: bool = False, resid: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """x [..., K] bf16, quantised along K in the call, through a linear layer whose weight
+    [N, K] is held in 8 bits: act(x W^T + bias) + resid [..., N] bf16."""
+    N, K = w.rows, w.K
+    px, ldx, M = _rows(x, "x", K, torch.bfloat16)
+    pw, ldw, sw = _fp8(w, "w")
+    if out is None:
+        out = torch.empty(*x.shape[:-1], N, dtype=torch.bfloat16, device=x.device)
+    po, ldo, _ = _rows(out, "out", N, torch.bfloat16, M)
+    pr, ldr = (None, N) if resid is None else _rows(resid, "resid", N, torch.bfloat16, M)[:2]
+    n = 0 if ws is not None else lib().rs_fp8_linear_ws_bytes(M, K)
+    pws, nws, ws = _ws(n, x.device, ws)
+    _check(lib().rs_fp8_linear(px, ldx, M, K, N, pw, ldw, sw,
+                               _vec(bias, "bias", N, torch.bfloat16), int(gelu), pr, ldr, po, ldo,
+                               pws, nws, _stream(stream)), "rs_fp8_linear")
+    return out
+
+
+def rs_fp8_linear_backward(dy: torch.Tensor, xt: Optional[Fp8], wt: Optional[Fp8],
+                           bias: bool = False, dw_dtype: torch.dtype = torch.bfloat16,
+                           ws: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of out = x W^T + bias for dy [M, N] bf16, from the transposed quantised
+    operands (rs_fp8_quantize(..., cols=True)): xt of x, [K, M], and wt of W, [K, N]. Returns
+    (dx [M, K] bf16, dw [N, K], db [N] fp32), None for dx without wt, dw without xt and db
+    without `bias`."""
+    N = dy.shape[-1]
+    pdy, lddy, M = _rows(dy, "dy", dtype=torch.bfloat16)
+    if xt is None and wt is None:
+        raise ValueError("xt or wt wanted")
+    K = xt.rows if xt is not None else wt.rows
+    dev = dy.device
+    px, ldx, sx = _fp8(xt, "xt", K, M) if xt is not None else (None, 0, None)
+    pw, ldw, sw = _fp8(wt, "wt", K, N) if wt is not None else (None, 0, None)
+    if dw_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("dw_dtype: bfloat16 or float32")
+    dx = torch.empty(*dy.shape[:-1], K, dtype=torch.bfloat16, device=dev) if wt is not None else None
+    dw = torch.empty(N, K, dtype=dw_dtype, device=dev) if xt is not None else None
+    db = torch.empty(N, dtype=torch.float32, device=dev) if bias else None
+    n = 0 if ws is not None else lib().rs_fp8_linear_backward_ws_bytes(M, N)
+    pws, nws, ws = _ws(n, dev, ws)
+    _check(lib().rs_fp8_linear_backward(pdy, lddy, M, N, K, px, ldx, sx, pw, ldw, sw,
+                                        None if dx is None else dx.data_ptr() or None, K,
+                                        None if dw is None else dw.data_ptr(), K,
+                                        _DTYPES[dw_dtype], None if db is None else db.data_ptr(),
+                                        pws, nws, _stream(stream)), "rs_fp8_linear_backward")
+    return dx, dw, db
+
+
+def rs_mlp_forward_fp8(x: torch.Tensor, w1: Fp8, b1, w2: Fp8, b2, gamma, beta,
+                       out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """rs_mlp_forward with W1 [H, C] and W2 [C, H] held in 8-bit blocks and both products in 8
+    bits: x [..., C] bf16 -> x + MLP(LN(x)), same shape."""
+    C, H = w1.K, w1.rows
+    px, ldx, M = _rows(x, "x", C, torch.bfloat16)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    p1, ld1, s1 = _fp8(w1, "w1")
+    p2, ld2, s2 = _fp8(w2, "w2", C, H)
+    if out is None:
+        out = torch.empty_like(x)
+    elif not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    bf = torch.bfloat16
+    n = 0 if ws is not None else lib().rs_mlp_forward_fp8_ws_bytes(M, C, H)
+    pws, nws, ws = _ws(n, x.device, ws)
+    st = lib().rs_mlp_forward_fp8(px, M, C, H, p1, ld1, s1, _vec(b1, "b1", H, bf), p2, ld2, s2,
+                                  _vec(b2, "b2", C, bf), _vec(gamma, "gamma", C, bf),
+                                  _vec(beta, "beta", C, bf), _rows(out, "out", C, bf, M)[0], pws,
+                                  nws, _stream(stream))
+    _check(st, "rs_mlp_forward_fp8")
+    return out

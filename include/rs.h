@@ -75,6 +75,13 @@ extern "C" {
  * 0 <= keep_k <= L, and kept_idx / y_kept hold keep_k entries per sample
  * instead of 1 + keep_k with the CLS token first. */
 #define RS_NO_CLS 1
+/* Element types of the layer norm and 8-bit entry points (rs_ln_forward and below).
+ * RS_E4M3: 8-bit blocks (rs_fp8_quantize), only as an output type of rs_fp8_gemm. */
+#define RS_BF16 0
+#define RS_FP16 1
+#define RS_FP32 2
+#define RS_E4M3 3
+#define RS_MAX_LN_C 8192
 
 typedef enum rs_status {
   RS_OK = 0,
@@ -86,7 +93,8 @@ typedef enum rs_status {
   RS_ERR_CUDA = 5,            /* the CUDA runtime or driver reported an error */
   RS_ERR_DEVICE_TIMEOUT = 6,  /* a kernel gave up waiting on its pipeline (device flag) */
   RS_ERR_NO_MEM = 7           /* the workspace could not be allocated, or would have to
-                                 grow on a stream that is being captured */
+                                 grow on a stream that is being captured, or the caller's
+                                 workspace is smaller than the call needs */
 } rs_status;
 
 /*
@@ -370,6 +378,123 @@ int rs_ln_fc1_gelu_noalloc(const void* x, int M, int C, int H, const void* W1, c
 int rs_debug_fc1_skip_load(const void* x, int M, int C, int H, const void* W1, const void* b1,
                            const void* gamma, const void* beta, void* hidden, int skip_kblock,
                            int timeout_us, void* stream);
+
+/*
+ * Layer norm, and products in 8 bits. The paper has no counterpart: these are the block's
+ * LayerNorm (Eq. (6)) written out with its gradients, and the block's two products with both
+ * operands in 8 bits, forward and backward.
+ *
+ * Conventions of this group, where they differ from the ones at the top:
+ *   - Rows may be strided: `ld...` is the distance between rows in elements (bytes for 8-bit
+ *     rows), at least the row's width; the elements of a row are contiguous. Tensors need the
+ *     alignment of their element type only, unless stated; rows that all start on 16 bytes
+ *     and are a whole number of 16-byte vectors run fastest.
+ *   - There is no library workspace: calls that need scratch take `ws` (256-byte aligned) and
+ *     `ws_bytes`, at least what the matching _ws_bytes function says (0 if the sizes are
+ *     invalid). Scratch holds nothing between calls, so calls with their own scratch may
+ *     overlap on any streams and be captured into any graphs.
+ *   - 0 <= rows < 2^27; other sizes as stated. Without rows nothing is launched except what
+ *     sets gradient sums to zero.
+ *   - Outputs may not overlap inputs except where stated.
+ *   - Infinities and NaN in an input go where the formulas send them.
+ */
+
+/* Layer norm: mean = sum x / C, var = sum (x - mean)^2 / C, rstd = 1/sqrt(var + eps),
+ * y = (x - mean) rstd gamma + beta, each row in fp32, y rounded once to x's type.
+ *   x [M, C], y [M, C]   `dtype` RS_BF16, RS_FP16 or RS_FP32; y may be x
+ *   gamma, beta [C]      `param_dtype` RS_FP32 or x's type; NULL for ones / zeros
+ *   stats [M, 2] fp32    (mean, rstd) per row for rs_ln_backward, or NULL (8-byte aligned)
+ * 1 <= C <= RS_MAX_LN_C, eps > 0. */
+int rs_ln_forward(const void* x, int64_t ldx, int M, int C, int dtype, const void* gamma,
+                  const void* beta, int param_dtype, float eps, void* y, int64_t ldy,
+                  float* stats, void* stream);
+
+/* The same norm with its output in 8-bit blocks along C (see rs_fp8_quantize), quantised from
+ * fp32: q [M, ldq] with ldq >= C a multiple of 16, scales as rs_fp8_scale_bytes(M, C) says.
+ * x RS_BF16 or RS_FP16, C a multiple of 8, x and parameters 16-byte aligned and ldx a multiple
+ * of 8; q 16-byte aligned. Bytes of q past C are left as they were. */
+int rs_ln_quantize(const void* x, int64_t ldx, int M, int C, int dtype, const void* gamma,
+                   const void* beta, int param_dtype, float eps, void* q, int64_t ldq,
+                   void* scales, float* stats, void* stream);
+
+/* Gradients of rs_ln_forward. With xh = (x - mean) rstd from `stats` and w = dy gamma:
+ *   dx     = rstd (w - mean_c(w) - xh mean_c(w xh)) + dres   [M, C], dtype (NULL: not computed)
+ *   dgamma = sum over rows of dy xh, dbeta = sum over rows of dy   [C] fp32 (either NULL)
+ * dy, x, dres [M, C] of `dtype`; dres is the gradient that reaches x past the norm (the
+ * residual stream's), or NULL; dx may be dres. gamma as for rs_ln_forward. The sums run in
+ * fp32 in an order that the sizes fix: a call gives the same bits every time. */
+int rs_ln_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* dres,
+                   int64_t lddres, const float* stats, const void* gamma, int param_dtype, int M,
+                   int C, int dtype, void* dx, int64_t lddx, float* dgamma, float* dbeta, void* ws,
+                   uint64_t ws_bytes, void* stream);
+uint64_t rs_ln_backward_ws_bytes(int M, int C);
+
+/* 8-bit blocks. A matrix [rows, K] is held as q [rows, ldq] e4m3 (ldq >= K a multiple of 16,
+ * 16-byte aligned) and one power-of-two scale 2^e per 128 consecutive values of a row (the
+ * last block of a row may be short): e is the least integer, at least -127, with
+ * max |x| <= 448 * 2^e over the block's finite values, and q = x * 2^-e rounded once, to
+ * nearest, ties to even. Infinities and NaN become NaN. The scale byte is e + 127, and row r,
+ * block j has its byte at
+ *   ((r / 128) KQ + j / 4) 512 + 16 (r % 32) + 4 (r / 32 % 4) + j % 4,  KQ = ceil(K / 512),
+ * of `scales`, rs_fp8_scale_bytes(rows, K) bytes (16-byte aligned); bytes of rows or blocks
+ * that do not exist are not written and not used. */
+uint64_t rs_fp8_scale_bytes(int rows, int K);
+
+/* x [rows, K] of `dtype` to 8-bit blocks along its rows (q, scales), and/or its transpose
+ * [K, rows] in blocks along the rows (qt with ldqt >= rows, scales_t), and/or its column sums
+ * colsum [K] fp32 (only together with qt; the one output that needs ws). NULL leaves an output
+ * out. Bytes of q and qt between a row's end and the next multiple of 16 may be set to zero. */
+int rs_fp8_quantize(const void* x, int64_t ldx, int rows, int K, int dtype, void* q, int64_t ldq,
+                    void* scales, void* qt, int64_t ldqt, void* scales_t, float* colsum, void* ws,
+                    uint64_t ws_bytes, void* stream);
+uint64_t rs_fp8_quantize_ws_bytes(int rows, int K);
+
+/* out [M, N] = act(A B^T + bias) + resid for A [M, K] and B [N, K] in 8-bit blocks along K:
+ * products of the stored values, accumulated in fp32 (in the tensor cores).
+ *   bias [N] bf16 or NULL (16-byte aligned); gelu: 1 for the exact GELU, 0 for none
+ *   resid [M, N] of out's type or NULL (added after act; may be out; not with RS_E4M3)
+ *   out: `out_dtype` RS_BF16, RS_FP32, or RS_E4M3, which stores 8-bit blocks along N (ldo a
+ *   multiple of 16, scales to out_scales, else NULL; bytes from a row's end to the next
+ *   multiple of 16 may be set to zero)
+ * A tcgen05 kernel; 1 <= N, K < 2^27. */
+int rs_fp8_gemm(const void* a, int64_t lda, const void* scales_a, const void* b, int64_t ldb,
+                const void* scales_b, int M, int N, int K, const void* bias, int gelu,
+                const void* resid, int64_t ldr, void* out, int64_t ldo, int out_dtype,
+                void* out_scales, void* stream);
+
+/* A linear layer with its weight held in 8 bits: x [M, K] bf16 is quantised along K, then
+ * out [M, N] bf16 = act(x W^T + bias) + resid as rs_fp8_gemm. wq [N, ldw], scales_w: W [N, K]
+ * in 8-bit blocks. */
+int rs_fp8_linear(const void* x, int64_t ldx, int M, int K, int N, const void* wq, int64_t ldw,
+                  const void* scales_w, const void* bias, int gelu, const void* resid, int64_t ldr,
+                  void* out, int64_t ldo, void* ws, uint64_t ws_bytes, void* stream);
+uint64_t rs_fp8_linear_ws_bytes(int M, int K);
+
+/* Gradients of out = x W^T + bias for the output gradient dy [M, N] bf16, both products in 8
+ * bits with blocks along what they reduce:
+ *   dx [M, K] bf16 = dy W      (dy in blocks along N, and W^T: wt [K, ldwt], scales_wt, the
+ *                              transposed output of rs_fp8_quantize for W [N, K])
+ *   dw [N, K]      = dy^T x    (dy^T in blocks along M, and x^T: xt [K, ldxt], scales_xt, the
+ *                              transposed output for x [M, K]); dw_dtype RS_BF16 or RS_FP32
+ *   db [N] fp32    = sum over rows of dy
+ * NULL outputs are not computed (their operands may then be NULL). */
+int rs_fp8_linear_backward(const void* dy, int64_t lddy, int M, int N, int K, const void* xt,
+                           int64_t ldxt, const void* scales_xt, const void* wt, int64_t ldwt,
+                           const void* scales_wt, void* dx, int64_t lddx, void* dw, int64_t lddw,
+                           int dw_dtype, float* db, void* ws, uint64_t ws_bytes, void* stream);
+uint64_t rs_fp8_linear_backward_ws_bytes(int M, int N);
+
+/* rs_mlp_forward with both products in 8 bits: y = x + fc2(GELU(fc1(LN(x)))), LN(x) and the
+ * hidden activation quantised as they are produced. Three launches: rs_ln_quantize (eps 1e-6),
+ * rs_fp8_gemm with GELU and RS_E4M3 output, rs_fp8_gemm with the residual.
+ *   x, y [M, C] bf16 contiguous, 16-byte aligned, y may be x; w1q [H, ldw1], w2q [C, ldw2]
+ *   with their scales: W1 [H, C] and W2 [C, H] in 8-bit blocks; b1, b2, gamma, beta bf16
+ * C and H as for rs_mlp_forward. */
+int rs_mlp_forward_fp8(const void* x, int M, int C, int H, const void* w1q, int64_t ldw1,
+                       const void* scales_w1, const void* b1, const void* w2q, int64_t ldw2,
+                       const void* scales_w2, const void* b2, const void* gamma, const void* beta,
+                       void* y, void* ws, uint64_t ws_bytes, void* stream);
+uint64_t rs_mlp_forward_fp8_ws_bytes(int M, int C, int H);
 
 /* Human-readable name of a status code (static storage). */
 const char* rs_status_string(int status);
