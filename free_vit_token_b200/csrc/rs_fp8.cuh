@@ -67,6 +67,7 @@ struct Elem;
 template <>
 struct Elem<__nv_bfloat16> {
   static constexpr int E = 8;
+  static constexpr bool kBf16 = true;
   static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -74,6 +75,12 @@ struct Elem<__nv_bfloat16> {
       f[2 * e] = bf16lo(w[e]);
       f[2 * e + 1] = bf16hi(w[e]);
     }
+  }
+  static __device__ __forceinline__ void pairs(const uint4& v, uint64_t (&f)[4]) {
+    f[0] = bf16x2_to_f2(v.x);
+    f[1] = bf16x2_to_f2(v.y);
+    f[2] = bf16x2_to_f2(v.z);
+    f[3] = bf16x2_to_f2(v.w);
   }
   static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
@@ -83,6 +90,7 @@ struct Elem<__nv_bfloat16> {
 template <>
 struct Elem<__half> {
   static constexpr int E = 8;
+  static constexpr bool kBf16 = false;
   static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -90,6 +98,14 @@ struct Elem<__half> {
       const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
       f[2 * e] = t.x;
       f[2 * e + 1] = t.y;
+    }
+  }
+  static __device__ __forceinline__ void pairs(const uint4& v, uint64_t (&f)[4]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+      f[e] = f2pack(t.x, t.y);
     }
   }
   static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
@@ -110,6 +126,10 @@ struct Elem<float> {
     f[1] = __uint_as_float(v.y);
     f[2] = __uint_as_float(v.z);
     f[3] = __uint_as_float(v.w);
+  }
+  static __device__ __forceinline__ void pairs(const uint4& v, uint64_t (&f)[2]) {
+    f[0] = (static_cast<uint64_t>(v.y) << 32) | v.x;
+    f[1] = (static_cast<uint64_t>(v.w) << 32) | v.z;
   }
   static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),

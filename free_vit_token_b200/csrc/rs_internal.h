@@ -283,12 +283,14 @@ struct Quant {
   uint8_t* qt;         // [K][ldqt] or null
   int64_t ldqt;
   uint8_t* scales_t;
-  float* partials;     // [quant_chunks(rows)][K] column sums, or null
+  float* partials;     // [quant_chunks(rows, K)][K] column sums, or null
 };
-// Row tiles of 128 are shared out over this many blocks per column tile.
-inline int quant_chunks(int rows) {
-  const int tiles = (rows + 127) / 128;
-  return tiles < 64 ? tiles : 64;
+// Blocks that share out the row tiles of 128 of one column tile: about four per SM in all (two
+// are resident, and a block loads its next tile while it works on one).
+inline int quant_chunks(int rows, int K) {
+  const int tiles = (rows + 127) / 128, cols = (K + 127) / 128;
+  const int most = cols < 592 ? (592 + cols - 1) / cols : 1;
+  return tiles < most ? tiles : most;
 }
 cudaError_t launch_quantize(const Quant& p, int dtype, bool vec, cudaStream_t s, bool pdl = false);
 

@@ -9,10 +9,17 @@
 //             dgamma = sum_rows dy xh, dbeta = sum_rows dy.
 //
 // All three are bound by memory. TPR threads own a row and hold it in registers (VPL 16-byte
-// vectors each), the next row's loads are issued before the current row is reduced, and every
-// value is read once. Backward: a thread keeps its columns' dgamma and dbeta sums in fp32
-// registers over all the rows of its block, the blocks' sums go to the workspace once each
-// and a second kernel adds them in a fixed order: no atomics, the same bits every run.
+// vectors each); blocks stay resident and walk the rows, and each row of threads keeps the
+// next rows on their way into a ring in shared memory (cp.async), so that the bytes in flight
+// do not depend on registers. Every value is read once, gamma and beta once per block.
+// Arithmetic runs on pairs of fp32 lanes. Backward: a thread keeps its columns' dgamma and
+// dbeta sums in fp32 registers over all the rows of its block, the blocks' sums go to the
+// workspace once each and a second kernel adds them in a fixed order: no atomics, the same bits
+// every run.
+//
+// Rows that do not start on 16 bytes (VEC = false) are copied as the aligned 16-byte units
+// that cover them and shifted into place between shared memory and registers, both ways, so
+// that global memory sees the same wide accesses.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -24,98 +31,235 @@
 
 namespace rs {
 
-// Where element e of vector i of thread l sits in a row. VEC: 16-byte vectors, vector
-// l + TPR i. Otherwise (a width, stride or address that is no multiple of 16 bytes)
-// neighbouring threads take neighbouring elements, so that narrow accesses still coalesce.
-template <typename T, int TPR, bool VEC>
-__device__ __forceinline__ int col_of(int l, int i, int e) {
-  constexpr int E = Elem<T>::E;
-  return VEC ? (l + TPR * i) * E + e : l + TPR * (i * E + e);
+// ---------------------------------------------------------------- rows
+// Element e of vector i of thread l is column (l + TPR i) E + e.
+template <typename T, int TPR>
+__device__ __forceinline__ int col_of(int l, int i) {
+  return (l + TPR * i) * Elem<T>::E;
 }
 
-template <typename T, int TPR, int VPL, bool VEC>
-__device__ __forceinline__ void load_row(const T* row, int C, int l, uint4 (&v)[VPL]) {
-  constexpr int E = Elem<T>::E;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    v[i] = make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The threads of a row meet.
+template <int TPR>
+__device__ __forceinline__ void group_barrier(int group) {
+  if constexpr (TPR <= 32)
+    __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(TPR) : "memory");
+}
+
+// A strided matrix of T, and how its rows lie against 16-byte boundaries.
+template <typename T, bool VEC>
+struct Rows {
+  const T* p;
+  int64_t ld;
+  int M, C;
+  __device__ __forceinline__ const T* row(int r) const { return p + static_cast<int64_t>(r) * ld; }
+  __device__ __forceinline__ int off(int r) const {
+    return VEC ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(row(r)) & 15);
+  }
+  // Row r to `buf` (TPR * VPL + 1 units of 16 bytes) asynchronously. With VEC thread l copies
+  // exactly what it reads; else the units at a row's ends come with the neighbouring rows'
+  // bytes, which nothing uses, and only a unit that would pass an end of the tensor moves by
+  // elements.
+  template <int TPR, int VPL>
+  __device__ __forceinline__ void fetch(uint8_t* buf, int r, int l) const {
+    const int len = C * static_cast<int>(sizeof(T));
     if constexpr (VEC) {
-      const int c = col_of<T, TPR, VEC>(l, i, 0);
-      if (c < C) v[i] = *reinterpret_cast<const uint4*>(row + c);
-    } else {
-      uint32_t w[4] = {0, 0, 0, 0};
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(row(r));
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int c = col_of<T, TPR, VEC>(l, i, e);
-        if (c < C) {
-          if constexpr (E == 8)
-            w[e / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(row)[c])
-                        << (16 * (e & 1));
-          else
-            w[e] = reinterpret_cast<const uint32_t*>(row)[c];
+      for (int i = 0; i < VPL; ++i) {
+        const int o = (l + TPR * i) * 16;
+        if (o < len) cp_async16(buf + o, src + o);
+      }
+    } else {
+      const int of = off(r);
+      const uint8_t* base = reinterpret_cast<const uint8_t*>(row(r)) - of;
+      const uint8_t* lo = reinterpret_cast<const uint8_t*>(p);
+      const uint8_t* hi = reinterpret_cast<const uint8_t*>(row(M - 1) + C);
+#pragma unroll
+      for (int i = 0; i <= VPL; ++i) {
+        const int o = (l + TPR * i) * 16;
+        if (o >= of + len) break;
+        if (base + o >= lo && base + o + 16 <= hi) {
+          cp_async16(buf + o, base + o);
+        } else {
+#pragma unroll 1
+          for (int b = o > of ? o : of; b < o + 16 && b < of + len; b += static_cast<int>(sizeof(T)))
+            *reinterpret_cast<T*>(buf + b) = *reinterpret_cast<const T*>(base + b);
         }
       }
-      v[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
+  }
+};
+
+// Vector i of thread l of a row at byte `of` of `buf`; zero past C.
+template <typename T, int TPR, bool VEC>
+__device__ __forceinline__ uint4 read_vec(const uint8_t* buf, int of, int C, int l, int i) {
+  constexpr int E = Elem<T>::E;
+  const int c = col_of<T, TPR>(l, i);
+  if (c >= C) return make_uint4(0, 0, 0, 0);
+  const uint4* unit = reinterpret_cast<const uint4*>(buf) + l + TPR * i;
+  const uint4 a = unit[0];
+  if constexpr (VEC) {
+    return a;
+  } else {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, 0, 0, 0, 0};
+    if (of != 0) {  // the same for all threads of the row
+      const uint4 b = unit[1];
+      w[4] = b.x;
+      w[5] = b.y;
+      w[6] = b.z;
+      w[7] = b.w;
+      if (of & 8) {
+#pragma unroll
+        for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
+      }
+      if (of & 4) {
+#pragma unroll
+        for (int j = 0; j < 5; ++j) w[j] = w[j + 1];
+      }
+      if (of & 2) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], 16);
+      }
+    }
+    if (c + E > C) {  // the row ends inside the vector
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (E == 8) {
+          if (c + 2 * j >= C) w[j] = 0;
+          else if (c + 2 * j + 1 >= C) w[j] &= 0xFFFFu;
+        } else {
+          if (c + j >= C) w[j] = 0;
+        }
+      }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
+// An output row: VEC, straight to global memory; else to byte `of` of `buf` (the offset of the
+// row in global memory), from where flush_row writes whole 16-byte units.
 template <typename T, int TPR, bool VEC>
-__device__ __forceinline__ void store_vec(T* row, int C, int l, int i,
+__device__ __forceinline__ void write_vec(T* row, uint8_t* buf, int of, int C, int l, int i,
                                           const float (&f)[Elem<T>::E]) {
-  constexpr int E = Elem<T>::E;
+  const int c = col_of<T, TPR>(l, i);
+  if (c >= C) return;
   const uint4 v = Elem<T>::pack(f);
   if constexpr (VEC) {
-    const int c = col_of<T, TPR, VEC>(l, i, 0);
-    if (c < C) *reinterpret_cast<uint4*>(row + c) = v;
+    *reinterpret_cast<uint4*>(row + c) = v;
   } else {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int c = col_of<T, TPR, VEC>(l, i, e);
-      if (c < C) {
-        if constexpr (E == 8)
-          reinterpret_cast<uint16_t*>(row)[c] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
-        else
-          reinterpret_cast<uint32_t*>(row)[c] = w[e];
-      }
+    uint8_t* d = buf + of + (l + TPR * i) * 16;
+    if (of & 2) {  // 16-bit elements between words
+      *reinterpret_cast<uint16_t*>(d) = static_cast<uint16_t>(v.x);
+      *reinterpret_cast<uint32_t*>(d + 2) = __funnelshift_r(v.x, v.y, 16);
+      *reinterpret_cast<uint32_t*>(d + 6) = __funnelshift_r(v.y, v.z, 16);
+      *reinterpret_cast<uint32_t*>(d + 10) = __funnelshift_r(v.z, v.w, 16);
+      *reinterpret_cast<uint16_t*>(d + 14) = static_cast<uint16_t>(v.w >> 16);
+    } else {
+      uint32_t* w = reinterpret_cast<uint32_t*>(d);
+      w[0] = v.x;
+      w[1] = v.y;
+      w[2] = v.z;
+      w[3] = v.w;
     }
+  }
+}
+template <typename T, int TPR, int VPL>
+__device__ __forceinline__ void flush_row(T* row, const uint8_t* buf, int of, int C, int l) {
+  const int end = of + C * static_cast<int>(sizeof(T));
+  uint8_t* base = reinterpret_cast<uint8_t*>(row) - of;
+#pragma unroll
+  for (int i = 0; i <= VPL; ++i) {
+    const int o = (l + TPR * i) * 16;
+    if (o >= end) break;
+    if (o >= of && o + 16 <= end)
+      *reinterpret_cast<uint4*>(base + o) = *reinterpret_cast<const uint4*>(buf + o);
+  }
+  // the elements of the two units at the ends that belong to this row, one per thread
+  constexpr int S = static_cast<int>(sizeof(T)), N = 16 / S;
+  static_assert(TPR >= 2 * N, "threads for both ends");
+  const int head = of == 0 ? 0 : 16, tail = end & ~15;
+  const int b = l < N ? of + l * S : tail + (l - N) * S;
+  const bool mine = l < N ? b < head && b < end : l < 2 * N && b < end && tail >= head;
+  if (mine && (l < N || b >= of)) *reinterpret_cast<T*>(base + b) = *reinterpret_cast<const T*>(buf + b);
+}
+
+// gamma or beta in pairs of fp32; 1 or 0 where there is none.
+template <typename T, bool VEC, bool P32>
+__device__ __forceinline__ void param_pairs(const void* p, float def, int c, int C,
+                                            uint64_t (&f)[Elem<T>::E / 2]) {
+  constexpr int E = Elem<T>::E;
+  if (p == nullptr) {
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) f[e] = f2pack(def, def);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) {
+    float v[2] = {0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (c + 2 * e + k < C)
+        v[k] = P32 ? __ldg(static_cast<const float*>(p) + c + 2 * e + k)
+                   : static_cast<float>(static_cast<const T*>(p)[c + 2 * e + k]);
+    f[e] = f2pack(v[0], v[1]);
   }
 }
 
-// gamma or beta for vector i: T or fp32 in memory (p32), `def` where there is none.
-template <typename T, int TPR, bool VEC>
-__device__ __forceinline__ void load_param(const void* p, bool p32, float def, int C, int l, int i,
-                                           float (&f)[Elem<T>::E]) {
-  constexpr int E = Elem<T>::E;
+// A block's copy of gamma or beta: 16-bit ones of aligned rows stay in registers as they are
+// (REGS), others are pairs of fp32 in shared memory, [VPL * E / 2][TPR].
+template <typename T, int TPR, int VPL, bool VEC, bool P32, bool REGS>
+struct Params {
+  static constexpr int E = Elem<T>::E;
+  const void* p;
+  float def;
+  const uint64_t* s;
+  uint4 raw[REGS ? VPL : 1];
+  // `s_` [VPL * E / 2][TPR] is filled by the block's first row of threads; the caller puts a
+  // __syncthreads between this and get().
+  __device__ __forceinline__ Params(const void* p_, float def_, int C, int group, int l, uint64_t* s_)
+      : p(p_), def(def_), s(s_ + l) {
+    if constexpr (REGS) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) f[e] = def;
-  if (p == nullptr) return;
-  if constexpr (VEC) {
-    const int c = col_of<T, TPR, VEC>(l, i, 0);
-    if (c >= C) return;
-    if (p32 || sizeof(T) == 4) {
-#pragma unroll
-      for (int e = 0; e < E; e += 4) {
-        const float4 g = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c + e));
-        f[e] = g.x;
-        f[e + 1] = g.y;
-        f[e + 2] = g.z;
-        f[e + 3] = g.w;
+      for (int i = 0; i < VPL; ++i) {
+        const int c = col_of<T, TPR>(l, i);
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (p != nullptr && c < C) raw[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p) + c));
       }
-    } else {
-      Elem<T>::unpack(__ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p) + c)), f);
-    }
-  } else {
+    } else if (group == 0) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int c = col_of<T, TPR, VEC>(l, i, e);
-      if (c < C)
-        f[e] = p32 ? __ldg(static_cast<const float*>(p) + c)
-                   : static_cast<float>(static_cast<const T*>(p)[c]);
+      for (int i = 0; i < VPL; ++i) {
+        uint64_t f[E / 2];
+        param_pairs<T, VEC, P32>(p, def, col_of<T, TPR>(l, i), C, f);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) s_[(i * E / 2 + e) * TPR + l] = f[e];
+      }
     }
   }
-}
+  __device__ __forceinline__ void get(int i, uint64_t (&f)[E / 2]) const {
+    if constexpr (REGS) {
+      if (p == nullptr) {
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) f[e] = f2pack(def, def);
+      } else {
+        Elem<T>::pairs(raw[i], f);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) f[e] = s[(i * E / 2 + e) * TPR];
+    }
+  }
+};
 
 // Sum of v over the TPR threads that share a row, given to all of them. Rows wider than a
 // warp meet in shared memory at a barrier of their own; `par` alternates between two slots,
@@ -132,7 +276,7 @@ __device__ __forceinline__ float2 group_sum(float2 v, float2* red, int group, in
     float2* slot = red + (group * 2 + par) * W;
     const int w = (threadIdx.x % TPR) >> 5;
     if ((threadIdx.x & 31) == 0) slot[w] = v;
-    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(TPR) : "memory");
+    group_barrier<TPR>(group);
     v = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < W; ++i) {
@@ -143,88 +287,136 @@ __device__ __forceinline__ float2 group_sum(float2 v, float2* red, int group, in
   }
   return v;
 }
+template <int TPR>
+__device__ __forceinline__ float group_sum(float v, float2* red, int group, int& par) {
+  if constexpr (TPR > 32) return group_sum<TPR>(make_float2(v, 0.f), red, group, par).x;
+#pragma unroll
+  for (int o = (TPR < 32 ? TPR : 32) / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
 
-__host__ __device__ constexpr int ln_threads(int tpr) { return tpr > 256 ? tpr : 256; }
+__host__ __device__ constexpr int ring_row_bytes(int tpr, int vpl) { return (tpr * vpl + 1) * 16; }
 
 // ---------------------------------------------------------------- forward
-template <typename T, int TPR, int VPL, bool VEC, bool QUANT>
-__global__ void __launch_bounds__(ln_threads(TPR))
+// Two blocks of 256 threads per SM (wide rows: one of 512), 4 rows on their way per row of
+// threads: 128 KB in flight per SM at 1024 bf16 columns.
+__host__ __device__ constexpr int fwd_threads(int tpr) { return tpr > 256 ? tpr : 256; }
+constexpr int kFwdStages = 4;
+template <typename T, bool VEC, bool P32>
+__host__ __device__ constexpr bool fwd_param_regs() {
+  return VEC && (sizeof(T) == 4 || !P32);
+}
+template <typename T, int TPR, int VPL, bool VEC, bool P32>
+__host__ __device__ constexpr int fwd_smem() {
+  return fwd_threads(TPR) / TPR * kFwdStages * ring_row_bytes(TPR, VPL) +
+         (fwd_param_regs<T, VEC, P32>() ? 0 : 2 * VPL * Elem<T>::E * TPR * 4);
+}
+
+template <typename T, int TPR, int VPL, bool VEC, bool P32, bool QUANT>
+__global__ void __launch_bounds__(fwd_threads(TPR), TPR <= 256 ? 2 : 1)
     ln_fwd_kernel(const LnForward p) {
   constexpr int E = Elem<T>::E;
-  constexpr int GROUPS = ln_threads(TPR) / TPR;
+  constexpr int GROUPS = fwd_threads(TPR) / TPR;
+  constexpr int RB = ring_row_bytes(TPR, VPL);
+  constexpr bool REGS = fwd_param_regs<T, VEC, P32>();
   static_assert(!QUANT || (VEC && E == 8 && TPR >= 16), "16 threads hold a block of 128");
   __shared__ float2 red[TPR > 32 ? GROUPS * 2 * (TPR / 32) : 1];
+  extern __shared__ __align__(16) uint8_t s_dyn[];
+  uint64_t* s_par = reinterpret_cast<uint64_t*>(s_dyn + GROUPS * kFwdStages * RB);
   pdl_trigger();
   pdl_wait();
   const int group = threadIdx.x / TPR, l = threadIdx.x % TPR;
   const int C = p.C;
   const float inv_c = 1.0f / static_cast<float>(C);
-  // rows that share a warp advance together (TPR < 32), so that its shuffles stay whole
-  const int sub = TPR < 32 ? group % (32 / TPR) : 0;
-  const T* x = static_cast<const T*>(p.x);
-  int par = 0;
-  uint4 cur[VPL], nxt[VPL];
+  const Rows<T, VEC> x{static_cast<const T*>(p.x), p.ldx, p.M, C};
+  uint8_t* ring = s_dyn + group * kFwdStages * RB;
   const int step = static_cast<int>(gridDim.x) * GROUPS;
-  int base = static_cast<int>(blockIdx.x) * GROUPS + group - sub;
-  auto load = [&](int r, uint4 (&v)[VPL]) {
-    if (r < p.M) {
-      load_row<T, TPR, VPL, VEC>(x + static_cast<int64_t>(r) * p.ldx, C, l, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) v[i] = make_uint4(0, 0, 0, 0);
-    }
+  int row = static_cast<int>(blockIdx.x) * GROUPS + group;
+  auto fetch = [&](int r, int slot) {
+    if (r < p.M) x.template fetch<TPR, VPL>(ring + slot * RB, r, l);
+    cp_async_commit();
   };
-  if (base < p.M) load(base + sub, cur);
-  for (; base < p.M; base += step) {
-    const int row = base + sub;
-    if (base + step < p.M) load(row + step, nxt);
-    float2 s = make_float2(0.f, 0.f);  // two running sums; padding adds zero
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      float f[E];
-      Elem<T>::unpack(cur[i], f);
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        s.x += f[e];
-        s.y += f[e + 1];
-      }
-    }
-    s = group_sum<TPR>(make_float2(s.x + s.y, 0.f), red, group, par);
-    const float mean = s.x * inv_c;
-    float2 q = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      float f[E];
-      Elem<T>::unpack(cur[i], f);
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        if (col_of<T, TPR, VEC>(l, i, e) < C) {
-          const float d = f[e] - mean;
-          q.x = fmaf(d, d, q.x);
-        }
-        if (col_of<T, TPR, VEC>(l, i, e + 1) < C) {
-          const float d = f[e + 1] - mean;
-          q.y = fmaf(d, d, q.y);
-        }
-      }
-    }
-    q = group_sum<TPR>(make_float2(q.x + q.y, 0.f), red, group, par);
-    const float rstd = rsqrtf(q.x * inv_c + p.eps);
+  for (int i = 0; i < kFwdStages - 1; ++i) fetch(row + i * step, i);
+  const Params<T, TPR, VPL, VEC, P32, REGS> gamma(p.gamma, 1.f, C, group, l, s_par);
+  const Params<T, TPR, VPL, VEC, P32, REGS> beta(p.beta, 0.f, C, group, l, s_par + VPL * E / 2 * TPR);
+  if constexpr (!REGS) __syncthreads();
+  int par = 0, slot = 0;
+  // rows that share a warp (TPR < 32) go through the same steps, past the end too
+  const int sub = TPR < 32 ? group % (32 / TPR) : 0;
+  for (; row - sub < p.M; row += step) {
     const bool live = row < p.M;
-    if (live && l == 0 && p.stats != nullptr) p.stats[row] = make_float2(mean, rstd);
+    cp_async_wait<kFwdStages - 2>();
+    // not VEC: other threads copied parts of the row; and all of them are done with the slot
+    // that is refilled next
+    if constexpr (!VEC) group_barrier<TPR>(group);
+    fetch(row + (kFwdStages - 1) * step, slot == 0 ? kFwdStages - 1 : slot - 1);
+    uint8_t* buf = ring + slot * RB;
+    slot = slot + 1 == kFwdStages ? 0 : slot + 1;
+    uint4 cur[VPL];
+    const int xof = x.off(row);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      cur[i] = live ? read_vec<T, TPR, VEC>(buf, xof, C, l, i) : make_uint4(0, 0, 0, 0);
+    uint64_t s2 = 0;  // pairs of running sums; padding adds zero
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      float f[E], g[E], b[E];
-      Elem<T>::unpack(cur[i], f);
-      load_param<T, TPR, VEC>(p.gamma, p.p32, 1.f, C, l, i, g);
-      load_param<T, TPR, VEC>(p.beta, p.p32, 0.f, C, l, i, b);
+      uint64_t f[E / 2];
+      Elem<T>::pairs(cur[i], f);
 #pragma unroll
-      for (int e = 0; e < E; ++e) f[e] = fmaf((f[e] - mean) * rstd, g[e], b[e]);
+      for (int e = 0; e < E / 2; ++e) s2 = fadd2(s2, f[e]);
+    }
+    float2 t = f2unpack(s2);
+    const float mean = group_sum<TPR>(t.x + t.y, red, group, par) * inv_c;
+    const uint64_t nmean = f2pack(-mean, -mean);
+    uint64_t q2 = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      uint64_t f[E / 2];
+      Elem<T>::pairs(cur[i], f);
+      const int c = col_of<T, TPR>(l, i);
+      if (VEC ? c < C : c + E <= C) {
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          const uint64_t d = fadd2(f[e], nmean);
+          q2 = ffma2(d, d, q2);
+        }
+      } else if (!VEC && c < C) {
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          uint64_t d = fadd2(f[e], nmean);
+          if (c + 2 * e >= C) d = 0;
+          if (c + 2 * e + 1 >= C) d = static_cast<uint32_t>(d);
+          q2 = ffma2(d, d, q2);
+        }
+      }
+    }
+    t = f2unpack(q2);
+    const float var = group_sum<TPR>(t.x + t.y, red, group, par) * inv_c;
+    const float rstd = rsqrtf(var + p.eps);
+    const uint64_t rstd2 = f2pack(rstd, rstd);
+    if (live && l == 0 && p.stats != nullptr) p.stats[row] = make_float2(mean, rstd);
+    T* y = static_cast<T*>(p.y) + static_cast<int64_t>(row) * p.ldy;
+    const int yof = VEC ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(y) & 15);
+    if constexpr (!VEC && !QUANT) group_barrier<TPR>(group);  // the slot is read: y takes its place
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      uint64_t f2[E / 2], g[E / 2], b[E / 2];
+      float f[E];
+      Elem<T>::pairs(cur[i], f2);
+      gamma.get(i, g);
+      beta.get(i, b);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) {
+        const float2 v = f2unpack(ffma2(fmul2(fadd2(f2[e], nmean), rstd2), g[e], b[e]));
+        f[2 * e] = v.x;
+        f[2 * e + 1] = v.y;
+      }
       if constexpr (!QUANT) {
-        if (live) store_vec<T, TPR, VEC>(static_cast<T*>(p.y) + row * p.ldy, C, l, i, f);
+        if (live) write_vec<T, TPR, VEC>(y, buf, yof, C, l, i, f);
       } else {
         // 16 neighbouring threads hold 128 columns: one block
-        const int c = col_of<T, TPR, VEC>(l, i, 0);
+        const int c = col_of<T, TPR>(l, i);
         uint32_t a = 0;
         if (c < C) {
 #pragma unroll
@@ -249,103 +441,157 @@ __global__ void __launch_bounds__(ln_threads(TPR))
           uint2 o;
           o.x = e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
           o.y = e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
-          *reinterpret_cast<uint2*>(p.q + row * p.ldq + c) = o;
+          *reinterpret_cast<uint2*>(p.q + static_cast<int64_t>(row) * p.ldq + c) = o;
           if ((l & 15) == 0) p.scales[scale_offset(row, c >> 7, p.kq)] = static_cast<uint8_t>(byte);
         }
       }
     }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) cur[i] = nxt[i];
+    if constexpr (!VEC && !QUANT) {
+      group_barrier<TPR>(group);
+      if (live) flush_row<T, TPR, VPL>(y, buf, yof, C, l);
+    }
   }
+  cp_async_wait<0>();
 }
 
 // ---------------------------------------------------------------- backward
-// Threads of a block: as many whole rows as fit in 384 threads at 168 registers each (one
-// block per SM; a row's x, dy and dres and the next row's are in registers at once).
+// Threads of a block: as many whole rows as fit in 384 threads at 168 registers each; one
+// block per SM. Each row of threads keeps a ring of 3 rows (2 where those are too large) of x,
+// dy and dres: up to 200 KB in flight per SM.
 __host__ __device__ constexpr int bwd_threads(int tpr) { return tpr >= 256 ? tpr : 384 / tpr * tpr; }
+__host__ __device__ constexpr int bwd_stages(int tpr) { return tpr == 128 || tpr > 256 ? 2 : 3; }
+__host__ __device__ constexpr int bwd_ring_bytes(int tpr, int vpl) {
+  return bwd_threads(tpr) / tpr * bwd_stages(tpr) * 3 * ring_row_bytes(tpr, vpl);
+}
+template <typename T, int VPL, bool VEC, bool P32>
+__host__ __device__ constexpr bool bwd_param_regs() {
+  return VEC && (sizeof(T) == 4 || (!P32 && VPL <= 3));
+}
 
-template <typename T, int TPR, int VPL, bool VEC>
+template <typename T, int TPR, int VPL, bool VEC, bool P32>
 __global__ void __launch_bounds__(bwd_threads(TPR), 1)
     ln_bwd_kernel(const LnBackward p) {
   constexpr int E = Elem<T>::E;
   constexpr int GROUPS = bwd_threads(TPR) / TPR;
   constexpr int NA = VPL * E;  // columns of a thread
+  constexpr int RB = ring_row_bytes(TPR, VPL);
+  constexpr int STAGES = bwd_stages(TPR);
+  constexpr bool REGS = bwd_param_regs<T, VPL, VEC, P32>();
   static_assert(TPR >= 32, "a warp shares a row");
   __shared__ float2 red[TPR > 32 ? GROUPS * 2 * (TPR / 32) : 1];
-  extern __shared__ float s_acc[];  // [GROUPS / 2 rounded up][2][NA][TPR]
+  extern __shared__ __align__(16) uint8_t s_dyn[];
+  float* s_acc = reinterpret_cast<float*>(s_dyn);  // [GROUPS / 2][2][NA][TPR]
   pdl_trigger();
   pdl_wait();
   const int group = threadIdx.x / TPR, l = threadIdx.x % TPR;
   const int C = p.C;
   const float inv_c = 1.0f / static_cast<float>(C);
-  const T* x = static_cast<const T*>(p.x);
-  const T* dy = static_cast<const T*>(p.dy);
-  const T* dres = static_cast<const T*>(p.dres);
-  T* dx = static_cast<T*>(p.dx);
-  float dg[NA], db[NA];
-#pragma unroll
-  for (int k = 0; k < NA; ++k) dg[k] = db[k] = 0.f;
-  int par = 0;
-  uint4 xc[VPL], yc[VPL], rc[VPL], xn[VPL], yn[VPL], rn[VPL];
-  float2 st = make_float2(0.f, 0.f), st_n = st;
+  const Rows<T, VEC> x{static_cast<const T*>(p.x), p.ldx, p.M, C};
+  const Rows<T, VEC> dy{static_cast<const T*>(p.dy), p.lddy, p.M, C};
+  const Rows<T, VEC> dres{static_cast<const T*>(p.dres), p.lddres, p.M, C};
+  uint8_t* ring = s_dyn + group * STAGES * 3 * RB;
   const int step = static_cast<int>(gridDim.x) * GROUPS;
   int row = static_cast<int>(blockIdx.x) * GROUPS + group;
-  auto load = [&](int r, uint4 (&a)[VPL], uint4 (&b)[VPL], uint4 (&d)[VPL], float2& s) {
-    s = __ldg(p.stats + r);
-    load_row<T, TPR, VPL, VEC>(x + static_cast<int64_t>(r) * p.ldx, C, l, a);
-    load_row<T, TPR, VPL, VEC>(dy + static_cast<int64_t>(r) * p.lddy, C, l, b);
-    if (dres != nullptr)
-      load_row<T, TPR, VPL, VEC>(dres + static_cast<int64_t>(r) * p.lddres, C, l, d);
+  auto fetch = [&](int r, int slot) {
+    if (r < p.M) {
+      uint8_t* b = ring + slot * 3 * RB;
+      x.template fetch<TPR, VPL>(b, r, l);
+      dy.template fetch<TPR, VPL>(b + RB, r, l);
+      if (dres.p != nullptr) dres.template fetch<TPR, VPL>(b + 2 * RB, r, l);
+    }
+    cp_async_commit();
   };
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) rc[i] = rn[i] = make_uint4(0, 0, 0, 0);
-  if (row < p.M) load(row, xc, yc, rc, st);
+  for (int i = 0; i < STAGES - 1; ++i) fetch(row + i * step, i);
+  const Params<T, TPR, VPL, VEC, P32, REGS> gamma(
+      p.gamma, 1.f, C, group, l, reinterpret_cast<uint64_t*>(s_dyn + bwd_ring_bytes(TPR, VPL)));
+  if constexpr (!REGS) __syncthreads();
+  uint64_t dg2[NA / 2], db2[NA / 2];  // pairs of columns
+#pragma unroll
+  for (int k = 0; k < NA / 2; ++k) dg2[k] = db2[k] = 0;
+  int par = 0, slot = 0;
   for (; row < p.M; row += step) {
-    if (row + step < p.M) load(row + step, xn, yn, rn, st_n);
-    float2 s = make_float2(0.f, 0.f);  // sum w, sum w xh; padding has dy = 0
+    const float2 st = __ldg(p.stats + row);
+    cp_async_wait<STAGES - 2>();
+    // not VEC: other threads copied parts of the row; and all of them are done with the slot
+    // that is refilled next
+    if constexpr (!VEC) group_barrier<TPR>(group);
+    fetch(row + (STAGES - 1) * step, slot == 0 ? STAGES - 1 : slot - 1);
+    uint8_t* b = ring + slot * 3 * RB;
+    slot = slot + 1 == STAGES ? 0 : slot + 1;
+    uint4 xc[VPL], yc[VPL];
+    const int xof = x.off(row), yof = dy.off(row);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      float fx[E], fy[E], g[E];
-      Elem<T>::unpack(xc[i], fx);
-      Elem<T>::unpack(yc[i], fy);
-      load_param<T, TPR, VEC>(p.gamma, p.p32, 1.f, C, l, i, g);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float xh = (fx[e] - st.x) * st.y;
-        const float w = fy[e] * g[e];
-        s.x += w;
-        s.y = fmaf(w, xh, s.y);
-        dg[i * E + e] = fmaf(fy[e], xh, dg[i * E + e]);
-        db[i * E + e] += fy[e];
-      }
+      xc[i] = read_vec<T, TPR, VEC>(b, xof, C, l, i);
+      yc[i] = read_vec<T, TPR, VEC>(b + RB, yof, C, l, i);
     }
-    if (dx != nullptr) {
-      s = group_sum<TPR>(s, red, group, par);
-      const float m1 = s.x * inv_c, m2 = s.y * inv_c;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        float fx[E], fy[E], g[E], fr[E];
-        Elem<T>::unpack(xc[i], fx);
-        Elem<T>::unpack(yc[i], fy);
-        Elem<T>::unpack(rc[i], fr);
-        load_param<T, TPR, VEC>(p.gamma, p.p32, 1.f, C, l, i, g);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float xh = (fx[e] - st.x) * st.y;
-          fr[e] = fmaf(st.y, fmaf(-xh, m2, fmaf(fy[e], g[e], -m1)), fr[e]);
-        }
-        store_vec<T, TPR, VEC>(dx + static_cast<int64_t>(row) * p.lddx, C, l, i, fr);
-      }
-    }
+    const uint64_t nmean = f2pack(-st.x, -st.x), rstd = f2pack(st.y, st.y);
+    uint64_t w2 = 0, wx2 = 0;  // sum w, sum w xh; padding has dy = 0
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      xc[i] = xn[i];
-      yc[i] = yn[i];
-      rc[i] = rn[i];
+      uint64_t fx[E / 2], fy[E / 2], g[E / 2];
+      Elem<T>::pairs(xc[i], fx);
+      Elem<T>::pairs(yc[i], fy);
+      gamma.get(i, g);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) {
+        const uint64_t xh = fmul2(fadd2(fx[e], nmean), rstd);
+        const uint64_t w = fmul2(fy[e], g[e]);
+        w2 = fadd2(w2, w);
+        wx2 = ffma2(w, xh, wx2);
+        dg2[i * E / 2 + e] = ffma2(fy[e], xh, dg2[i * E / 2 + e]);
+        db2[i * E / 2 + e] = fadd2(db2[i * E / 2 + e], fy[e]);
+      }
     }
-    st = st_n;
+    if (p.dx == nullptr) continue;
+    const float2 wf = f2unpack(w2), wxf = f2unpack(wx2);
+    const float2 s = group_sum<TPR>(make_float2(wf.x + wf.y, wxf.x + wxf.y), red, group, par);
+    const float m1 = s.x * inv_c, m2 = s.y * inv_c;
+    const uint64_t nm1 = f2pack(-m1, -m1), nm2 = f2pack(-m2, -m2);
+    uint4 rc[VPL];
+    const int rof = dres.p != nullptr ? dres.off(row) : 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      rc[i] = dres.p != nullptr ? read_vec<T, TPR, VEC>(b + 2 * RB, rof, C, l, i)
+                                : make_uint4(0, 0, 0, 0);
+    T* dx = static_cast<T*>(p.dx) + static_cast<int64_t>(row) * p.lddx;
+    const int dof = VEC ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(dx) & 15);
+    if constexpr (!VEC) group_barrier<TPR>(group);  // dres is read: dx takes its place
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      uint64_t fx[E / 2], fy[E / 2], g[E / 2], fr[E / 2];
+      float o[E];
+      Elem<T>::pairs(xc[i], fx);
+      Elem<T>::pairs(yc[i], fy);
+      Elem<T>::pairs(rc[i], fr);
+      gamma.get(i, g);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) {
+        const uint64_t xh = fmul2(fadd2(fx[e], nmean), rstd);
+        const float2 v = f2unpack(ffma2(rstd, ffma2(xh, nm2, ffma2(fy[e], g[e], nm1)), fr[e]));
+        o[2 * e] = v.x;
+        o[2 * e + 1] = v.y;
+      }
+      write_vec<T, TPR, VEC>(dx, b + 2 * RB, dof, C, l, i, o);
+    }
+    if constexpr (!VEC) {
+      group_barrier<TPR>(group);
+      flush_row<T, TPR, VPL>(dx, b + 2 * RB, dof, C, l);
+    }
   }
+  cp_async_wait<0>();
+  __syncthreads();  // the ring becomes the sums' memory
   if (p.partials == nullptr) return;
+  float dg[NA], db[NA];
+#pragma unroll
+  for (int k = 0; k < NA / 2; ++k) {
+    const float2 a = f2unpack(dg2[k]), b = f2unpack(db2[k]);
+    dg[2 * k] = a.x;
+    dg[2 * k + 1] = a.y;
+    db[2 * k] = b.x;
+    db[2 * k + 1] = b.y;
+  }
   // the block's groups added pairwise in shared memory, the upper half into the lower
 #pragma unroll
   for (int n = GROUPS; n > 1;) {
@@ -376,7 +622,7 @@ __global__ void __launch_bounds__(bwd_threads(TPR), 1)
     for (int i = 0; i < VPL; ++i) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const int c = col_of<T, TPR, VEC>(l, i, e);
+        const int c = col_of<T, TPR>(l, i) + e;
         if (c < C) {
           out[c] = dg[i * E + e];
           out[C + c] = db[i * E + e];
@@ -418,13 +664,25 @@ cudaError_t launch_col_reduce(const float* partials, int P, int n, int split, fl
 }
 
 // ---------------------------------------------------------------- host launchers
+template <typename T, int TPR, int VPL, bool VEC, bool QUANT, bool P32>
+static cudaError_t go_fwd_p(const LnForward& p, int num_sms, cudaStream_t s) {
+  constexpr int groups = fwd_threads(TPR) / TPR;
+  constexpr int smem = fwd_smem<T, TPR, VPL, VEC, P32>();
+  static_assert(smem + 1024 <= 232448, "shared memory");
+  constexpr int per_sm = TPR <= 256 && 2 * (smem + 2048) <= 232448 ? 2 : 1;
+  auto kern = ln_fwd_kernel<T, TPR, VPL, VEC, P32, QUANT>;
+  if constexpr (smem > 40 * 1024) {  // with the static part past the default 48 KB
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  const int blocks = (p.M + groups - 1) / groups, most = per_sm * num_sms;
+  return launch(kern, dim3(blocks < most ? blocks : most), dim3(fwd_threads(TPR)), smem, s, false, p);
+}
 template <typename T, int TPR, int VPL, bool VEC, bool QUANT>
 static cudaError_t go_fwd(const LnForward& p, int num_sms, cudaStream_t s) {
-  constexpr int groups = ln_threads(TPR) / TPR;
-  const int64_t blocks = (static_cast<int64_t>(p.M) + groups - 1) / groups;
-  const int64_t most = static_cast<int64_t>(num_sms) * (2048 / ln_threads(TPR));
-  return launch(ln_fwd_kernel<T, TPR, VPL, VEC, QUANT>, dim3(blocks < most ? blocks : most),
-                dim3(ln_threads(TPR)), 0, s, false, p);
+  if constexpr (sizeof(T) == 4) return go_fwd_p<T, TPR, VPL, VEC, QUANT, true>(p, num_sms, s);
+  return p.p32 ? go_fwd_p<T, TPR, VPL, VEC, QUANT, true>(p, num_sms, s)
+               : go_fwd_p<T, TPR, VPL, VEC, QUANT, false>(p, num_sms, s);
 }
 
 // Threads per row by width, in 16-byte vectors of the row: narrow rows share a warp, so that
@@ -469,17 +727,26 @@ cudaError_t launch_ln_quantize(const LnForward& p, int dtype, int num_sms, cudaS
                           : pick_quant<__half>(p, num_sms, s);
 }
 
-template <typename T, int TPR, int VPL, bool VEC>
-static cudaError_t go_bwd(const LnBackward& p, int blocks, cudaStream_t s) {
-  constexpr int groups = bwd_threads(TPR) / TPR;
-  constexpr size_t smem = static_cast<size_t>(groups / 2) * 2 * VPL * Elem<T>::E * TPR * 4;
-  auto kern = ln_bwd_kernel<T, TPR, VPL, VEC>;
+template <typename T, int TPR, int VPL, bool VEC, bool P32>
+static cudaError_t go_bwd_p(const LnBackward& p, int blocks, cudaStream_t s) {
+  static_assert(bwd_threads(TPR) / TPR / 2 * 2 * VPL * Elem<T>::E * TPR * 4 <= bwd_ring_bytes(TPR, VPL),
+                "the sums fit the ring");
+  constexpr size_t smem = bwd_ring_bytes(TPR, VPL) +
+                          (bwd_param_regs<T, VPL, VEC, P32>() ? 0 : VPL * Elem<T>::E * TPR * 4);
+  static_assert(smem + 1024 <= 232448, "shared memory");
+  auto kern = ln_bwd_kernel<T, TPR, VPL, VEC, P32>;
   if constexpr (smem > 40 * 1024) {  // with the static part past the default 48 KB
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
   return launch(kern, dim3(blocks), dim3(bwd_threads(TPR)), smem, s, false, p);
+}
+template <typename T, int TPR, int VPL, bool VEC>
+static cudaError_t go_bwd(const LnBackward& p, int blocks, cudaStream_t s) {
+  if constexpr (sizeof(T) == 4) return go_bwd_p<T, TPR, VPL, VEC, true>(p, blocks, s);
+  return p.p32 ? go_bwd_p<T, TPR, VPL, VEC, true>(p, blocks, s)
+               : go_bwd_p<T, TPR, VPL, VEC, false>(p, blocks, s);
 }
 
 // Threads per row and vectors per thread, by the row's 16-byte vectors: at most 4 vectors a

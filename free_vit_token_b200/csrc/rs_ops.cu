@@ -223,7 +223,7 @@ uint64_t rs_fp8_scale_bytes(int rows, int K) {
 
 uint64_t rs_fp8_quantize_ws_bytes(int rows, int K) {
   if (rows < 0 || rows >= kMaxDim || !dim_ok(K)) return 0;
-  const uint64_t chunks = rows > 0 ? rs::quant_chunks(rows) : 1;
+  const uint64_t chunks = rows > 0 ? rs::quant_chunks(rows, K) : 1;
   return up(chunks * static_cast<uint64_t>(K) * 4, 256);
 }
 
@@ -260,7 +260,7 @@ int rs_fp8_quantize(const void* x, int64_t ldx, int rows, int K, int dtype, void
   const bool vec = aligned(x, 16) && ldx * es % 16 == 0 && K % 8 == 0;
   RS_CUDA(rs::launch_quantize(p, dtype, vec, s));
   if (colsum)
-    RS_CUDA(rs::launch_col_reduce(p.partials, rs::quant_chunks(rows), K, K, colsum, nullptr, s, true));
+    RS_CUDA(rs::launch_col_reduce(p.partials, rs::quant_chunks(rows, K), K, K, colsum, nullptr, s, true));
   return RS_OK;
 }
 
@@ -427,7 +427,7 @@ int rs_fp8_linear_backward(const void* dy, int64_t lddy, int M, int N, int K, co
     RS_TRY(gemm(p, dw_dtype, s, true));
   }
   if (db)
-    RS_CUDA(rs::launch_col_reduce(qp.partials, rs::quant_chunks(M), N, N, db, nullptr, s, true));
+    RS_CUDA(rs::launch_col_reduce(qp.partials, rs::quant_chunks(M, N), N, N, db, nullptr, s, true));
   return RS_OK;
 }
 

@@ -21,41 +21,97 @@ namespace rs {
 
 constexpr int kQTile = 128;
 
+// 8 neighbouring columns of a row as they lie in memory (16-bit types: 4 words of two, fp32:
+// 8 words) and what the kernel asks of them. Magnitudes order like their bits without the
+// sign, infinity above every finite value and NaN above infinity.
 template <typename T>
-__device__ __forceinline__ float elem_to_float(T v) { return static_cast<float>(v); }
+struct Cols8 {  // bf16, fp16
+  static constexpr int W = 4;
+  static constexpr uint32_t kInf = sizeof(T) == 2 && Elem<T>::kBf16 ? 0x7F80u : 0x7C00u;
+  uint32_t w[W];
+  static __device__ __forceinline__ uint32_t vmax(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+  __device__ __forceinline__ uint32_t mag(int i) const { return w[i] & 0x7FFF7FFFu; }
+  static __device__ __forceinline__ bool nonfinite(uint32_t m) {
+    return (m & 0xFFFFu) >= kInf || (m >> 16) >= kInf;
+  }
+  static __device__ __forceinline__ uint32_t finite_part(uint32_t m) {
+    return ((m & 0xFFFFu) >= kInf ? 0u : m & 0xFFFFu) | ((m >> 16) >= kInf ? 0u : m & 0xFFFF0000u);
+  }
+  __device__ __forceinline__ void inf_to_nan_all() {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      if ((w[i] & 0x7FFFu) == kInf) w[i] |= 0x7FFFu;
+      if (((w[i] >> 16) & 0x7FFFu) == kInf) w[i] |= 0x7FFF0000u;
+    }
+  }
+  // a word of magnitudes (of one column or two) as fp32 bits: the larger, or each half
+  static __device__ __forceinline__ uint32_t wide(uint32_t h) {
+    if constexpr (Elem<T>::kBf16) return h << 16;
+    return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(h))));
+  }
+  static __device__ __forceinline__ uint32_t top(uint32_t m) { return wide(max(m & 0xFFFFu, m >> 16)); }
+  static __device__ __forceinline__ uint32_t col(uint32_t m, int e) { return wide(e ? m >> 16 : m & 0xFFFFu); }
+  __device__ __forceinline__ float get(int e) const {
+    const uint32_t v = w[e >> 1];
+    if constexpr (Elem<T>::kBf16) return (e & 1) ? bf16hi(v) : bf16lo(v);
+    return __half2float(__ushort_as_half(static_cast<unsigned short>((e & 1) ? v >> 16 : v & 0xFFFFu)));
+  }
+};
+template <>
+struct Cols8<float> {
+  static constexpr int W = 8;
+  uint32_t w[W];
+  static __device__ __forceinline__ uint32_t vmax(uint32_t a, uint32_t b) { return max(a, b); }
+  __device__ __forceinline__ uint32_t mag(int i) const { return w[i] & 0x7FFFFFFFu; }
+  static __device__ __forceinline__ bool nonfinite(uint32_t m) { return m >= kInfBits; }
+  static __device__ __forceinline__ uint32_t finite_part(uint32_t m) { return m >= kInfBits ? 0u : m; }
+  __device__ __forceinline__ void inf_to_nan_all() {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if ((w[i] & 0x7FFFFFFFu) == kInfBits) w[i] = 0x7FFFFFFFu;
+  }
+  static __device__ __forceinline__ uint32_t top(uint32_t m) { return m; }
+  static __device__ __forceinline__ uint32_t col(uint32_t m, int) { return m; }
+  __device__ __forceinline__ float get(int e) const { return __uint_as_float(w[e]); }
+};
 
-// 8 neighbouring columns of a row, zero past K.
+// Zero past K (and for rows that do not exist).
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* row, int c, int K, float (&f)[8]) {
+__device__ __forceinline__ void load8(const T* row, int c, int K, bool live, Cols8<T>& v) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = 0.f;
+  for (int i = 0; i < Cols8<T>::W; ++i) v.w[i] = 0;
   if constexpr (VEC) {
-    if (c < K) {  // K is a multiple of 8
-      if constexpr (Elem<T>::E == 8) {
-        Elem<T>::unpack(*reinterpret_cast<const uint4*>(row + c), f);
-      } else {
-        float a[4], b[4];
-        Elem<T>::unpack(*reinterpret_cast<const uint4*>(row + c), a);
-        Elem<T>::unpack(*reinterpret_cast<const uint4*>(row + c + 4), b);
+    if (live && c < K) {  // K is a multiple of 8
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          f[e] = a[e];
-          f[4 + e] = b[e];
-        }
+      for (int i = 0; i < Cols8<T>::W; i += 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(row + c) + i);
+        v.w[i] = u.x;
+        v.w[i + 1] = u.y;
+        v.w[i + 2] = u.z;
+        v.w[i + 3] = u.w;
       }
     }
-  } else {
+  } else if (live) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c + e < K) f[e] = static_cast<float>(row[c + e]);
+    for (int e = 0; e < 8; ++e) {
+      if (c + e < K) {
+        if constexpr (sizeof(T) == 2)
+          v.w[e >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(row)[c + e]) << (16 * (e & 1));
+        else
+          v.w[e] = reinterpret_cast<const uint32_t*>(row)[c + e];
+      }
+    }
   }
 }
 
 template <typename T, bool VEC, bool ROWS, bool COLS>
-__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) quantize_kernel(const Quant p) {
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2) quantize_kernel(const Quant p) {
+  using V = Cols8<T>;
+  constexpr int CW = 8 / V::W;  // columns of a word
   __shared__ __align__(16) uint8_t s_t[COLS ? kQTile * kQTile : 16];
-  __shared__ uint32_t s_max[COLS ? 8 : 1][kQTile];
-  __shared__ float s_sum[8][COLS ? kQTile : 1];
+  __shared__ uint32_t s_max[COLS ? 8 : 1][COLS ? kQTile / CW : 1];
+  __shared__ uint32_t s_byte[COLS ? kQTile : 1];
+  __shared__ float s_sum[COLS ? 8 : 1][COLS ? kQTile : 1];
   pdl_trigger();
   pdl_wait();
   const int t = threadIdx.x, warp = t >> 5;
@@ -65,100 +121,114 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) quantize_kernel(c
   const int kq = (p.K + 511) / 512, kqt = (p.rows + 511) / 512;
   const T* x = static_cast<const T*>(p.x);
   float sum[8] = {};
-  for (int rt = blockIdx.y; rt < row_tiles; rt += gridDim.y) {
+  V v[8], nx[8];
+  auto load = [&](int rt, V (&d)[8]) {
     const int r0 = rt * kQTile + 8 * ty;
-    float f[8][8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (r0 + j < p.rows) {
-        load8<T, VEC>(x + static_cast<int64_t>(r0 + j) * p.ldx, c, p.K, f[j]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[j][e] = 0.f;
-      }
-    }
-    uint32_t bad = 0;  // any infinity or NaN of this thread
 #pragma unroll
     for (int j = 0; j < 8; ++j)
+      load8<T, VEC>(x + static_cast<int64_t>(r0 + j) * p.ldx, c, p.K, r0 + j < p.rows, d[j]);
+  };
+  int rt = blockIdx.y;
+  if (rt < row_tiles) load(rt, v);
+  for (; rt < row_tiles; rt += gridDim.y) {
+    if (rt + static_cast<int>(gridDim.y) < row_tiles) load(rt + gridDim.y, nx);
+    const int r0 = rt * kQTile + 8 * ty;
+    // the largest magnitude of each row (rm) and column (cm) of this thread's 8 x 8
+    uint32_t rm[8], cm[V::W], all = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        bad |= abs_bits(f[j][e]) >= kInfBits ? 1u : 0u;
-        if constexpr (COLS) sum[e] += f[j][e];
+    for (int i = 0; i < V::W; ++i) cm[i] = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      rm[j] = 0;
+#pragma unroll
+      for (int i = 0; i < V::W; ++i) {
+        const uint32_t m = v[j].mag(i);
+        rm[j] = V::vmax(rm[j], m);
+        if constexpr (COLS) cm[i] = V::vmax(cm[i], m);
       }
+      all = V::vmax(all, rm[j]);
+      if constexpr (COLS) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += v[j].get(e);
+      }
+    }
+    if (V::nonfinite(all)) {  // rare: infinities become NaN, and neither counts
+#pragma unroll
+      for (int i = 0; i < V::W; ++i) cm[i] = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j].inf_to_nan_all();
+        rm[j] = 0;
+#pragma unroll
+        for (int i = 0; i < V::W; ++i) {
+          const uint32_t m = V::finite_part(v[j].mag(i));
+          rm[j] = V::vmax(rm[j], m);
+          cm[i] = V::vmax(cm[i], m);
+        }
+      }
+    }
+    if constexpr (COLS) {
+#pragma unroll
+      for (int i = 0; i < V::W; ++i) cm[i] = V::vmax(cm[i], __shfl_xor_sync(0xffffffffu, cm[i], 16));
+      if ((t & 16) == 0) {
+#pragma unroll
+        for (int i = 0; i < V::W; ++i) s_max[warp][V::W * tx + i] = cm[i];
+      }
+      __syncthreads();
+      if (t < kQTile) {
+        uint32_t m = s_max[0][t / CW];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) m = V::vmax(m, s_max[w][t / CW]);
+        const uint32_t byte = e8m0_byte(V::col(m, t % CW));
+        s_byte[t] = byte;
+        if (c0 + t < p.K) p.scales_t[scale_offset(c0 + t, rt, kqt)] = static_cast<uint8_t>(byte);
+      }
+    }
     if constexpr (ROWS) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        uint32_t a = 0;
+        uint32_t m = rm[j];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          a = max(a, bad ? finite_abs_bits(f[j][e]) : abs_bits(f[j][e]));
-#pragma unroll
-        for (int o = 8; o; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-        const uint32_t byte = e8m0_byte(a);
+        for (int o = 8; o; o >>= 1) m = V::vmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const uint32_t byte = e8m0_byte(V::top(m));
         const float inv = e8m0_inverse(byte);
         const int r = r0 + j;
         if (r < p.rows && c < p.K) {
-          float v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = (bad ? inf_to_nan(f[j][e]) : f[j][e]) * inv;
           uint2 o;
-          o.x = e4m3x4(v[0], v[1], v[2], v[3]);
-          o.y = e4m3x4(v[4], v[5], v[6], v[7]);
+          o.x = e4m3x4(v[j].get(0) * inv, v[j].get(1) * inv, v[j].get(2) * inv, v[j].get(3) * inv);
+          o.y = e4m3x4(v[j].get(4) * inv, v[j].get(5) * inv, v[j].get(6) * inv, v[j].get(7) * inv);
           *reinterpret_cast<uint2*>(p.q + static_cast<int64_t>(r) * p.ldq + c) = o;
           if (tx == 0) p.scales[scale_offset(r, c0 >> 7, kq)] = static_cast<uint8_t>(byte);
         }
       }
     }
     if constexpr (COLS) {
-      uint32_t a[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        a[e] = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          a[e] = max(a[e], bad ? finite_abs_bits(f[j][e]) : abs_bits(f[j][e]));
-        a[e] = max(a[e], __shfl_xor_sync(0xffffffffu, a[e], 16));
-      }
-      if ((t & 16) == 0) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s_max[warp][8 * tx + e] = a[e];
-      }
-      __syncthreads();
-      if (t < kQTile) {
-        uint32_t m = s_max[0][t];
-#pragma unroll
-        for (int w = 1; w < 8; ++w) m = max(m, s_max[w][t]);
-        const uint32_t byte = e8m0_byte(m);
-        s_max[0][t] = byte;  // only this thread reads or writes column t here
-        if (c0 + t < p.K) p.scales_t[scale_offset(c0 + t, rt, kqt)] = static_cast<uint8_t>(byte);
-      }
       __syncthreads();
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float inv = e8m0_inverse(s_max[0][8 * tx + e]);
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = (bad ? inf_to_nan(f[j][e]) : f[j][e]) * inv;
+        const float inv = e8m0_inverse(s_byte[8 * tx + e]);
         uint2 o;
-        o.x = e4m3x4(v[0], v[1], v[2], v[3]);
-        o.y = e4m3x4(v[4], v[5], v[6], v[7]);
+        o.x = e4m3x4(v[0].get(e) * inv, v[1].get(e) * inv, v[2].get(e) * inv, v[3].get(e) * inv);
+        o.y = e4m3x4(v[4].get(e) * inv, v[5].get(e) * inv, v[6].get(e) * inv, v[7].get(e) * inv);
         *reinterpret_cast<uint2*>(s_t + (8 * tx + e) * kQTile + ((ty ^ tx) << 3)) = o;
       }
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int col = i * 32 + (t >> 3), ch = t & 7;  // 16 rows 16 ch .. of column col
+        const int col = i * 32 + (t >> 3), ch = t & 7;  // rows 16 ch .. of column col
         const int g = (2 * ch) ^ (col >> 3);
-        const uint4 v = *reinterpret_cast<const uint4*>(s_t + col * kQTile + ((g >> 1) << 4));
-        const uint4 o = (g & 1) ? make_uint4(v.z, v.w, v.x, v.y) : v;
+        const uint4 u = *reinterpret_cast<const uint4*>(s_t + col * kQTile + ((g >> 1) << 4));
+        const uint4 o = (g & 1) ? make_uint4(u.z, u.w, u.x, u.y) : u;
         const int r = rt * kQTile + 16 * ch;
         if (c0 + col < p.K && r < p.rows)
           *reinterpret_cast<uint4*>(p.qt + static_cast<int64_t>(c0 + col) * p.ldqt + r) = o;
       }
-      // the next tile's s_max and s_t are written only after every thread passes its first
-      // barrier, which no thread reaches before it has read s_t here; s_max[0] is rewritten
-      // before that barrier, and was last read before the one above
+      // Three barriers a tile order the shared arrays: s_max is written before the first and
+      // read before the second, s_byte written before the second and read before the third,
+      // s_t written before the third and read before the next tile's first.
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = nx[j];
   }
   if constexpr (COLS) {
     if (p.partials != nullptr) {
@@ -170,10 +240,10 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) quantize_kernel(c
       }
       __syncthreads();
       if (t < kQTile && c0 + t < p.K) {
-        float v = s_sum[0][t];
+        float a = s_sum[0][t];
 #pragma unroll
-        for (int w = 1; w < 8; ++w) v += s_sum[w][t];
-        p.partials[static_cast<int64_t>(blockIdx.y) * p.K + c0 + t] = v;
+        for (int w = 1; w < 8; ++w) a += s_sum[w][t];
+        p.partials[static_cast<int64_t>(blockIdx.y) * p.K + c0 + t] = a;
       }
     }
   }
@@ -182,16 +252,10 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) quantize_kernel(c
 template <typename T, bool VEC>
 static cudaError_t pick(const Quant& p, cudaStream_t s, bool pdl) {
   const dim3 block(256);
-  const int ct = (p.K + kQTile - 1) / kQTile;
-  if (p.qt != nullptr) {
-    const dim3 grid(ct, quant_chunks(p.rows));
-    if (p.q != nullptr) return launch(quantize_kernel<T, VEC, true, true>, grid, block, 0, s, pdl, p);
-    return launch(quantize_kernel<T, VEC, false, true>, grid, block, 0, s, pdl, p);
-  }
-  // rows only: nothing is carried from tile to tile, so each tile has a block of its own
-  const int tiles = (p.rows + kQTile - 1) / kQTile;
-  return launch(quantize_kernel<T, VEC, true, false>, dim3(ct, tiles < 65535 ? tiles : 65535), block,
-                0, s, pdl, p);
+  const dim3 grid((p.K + kQTile - 1) / kQTile, quant_chunks(p.rows, p.K));
+  if (p.qt == nullptr) return launch(quantize_kernel<T, VEC, true, false>, grid, block, 0, s, pdl, p);
+  if (p.q == nullptr) return launch(quantize_kernel<T, VEC, false, true>, grid, block, 0, s, pdl, p);
+  return launch(quantize_kernel<T, VEC, true, true>, grid, block, 0, s, pdl, p);
 }
 
 cudaError_t launch_quantize(const Quant& p, int dtype, bool vec, cudaStream_t s, bool pdl) {
