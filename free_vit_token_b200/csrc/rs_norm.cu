@@ -455,13 +455,17 @@ __global__ void __launch_bounds__(fwd_threads(TPR), TPR <= 256 ? 2 : 1)
 }
 
 // ---------------------------------------------------------------- backward
-// Threads of a block: as many whole rows as fit in 384 threads at 168 registers each; one
-// block per SM. Each row of threads keeps a ring of 3 rows (2 where those are too large) of x,
-// dy and dres: up to 200 KB in flight per SM.
-__host__ __device__ constexpr int bwd_threads(int tpr) { return tpr >= 256 ? tpr : 384 / tpr * tpr; }
-__host__ __device__ constexpr int bwd_stages(int tpr) { return tpr == 128 || tpr > 256 ? 2 : 3; }
-__host__ __device__ constexpr int bwd_ring_bytes(int tpr, int vpl) {
-  return bwd_threads(tpr) / tpr * bwd_stages(tpr) * 3 * ring_row_bytes(tpr, vpl);
+// Threads of a block (one per SM): 512 at 128 registers each where a thread's columns' sums (16
+// bytes each) leave room, else 384 at 168. Each row of threads keeps a ring of 3 rows (2 where
+// those are too large) of x, dy and dres: up to 200 KB in flight per SM.
+__host__ __device__ constexpr int bwd_threads(int tpr, int na) {
+  return na <= 16 || tpr == 512 ? 512 : 384 / tpr * tpr;
+}
+__host__ __device__ constexpr int bwd_stages(int tpr, int vpl, int na) {
+  return bwd_threads(tpr, na) / tpr * 9 * ring_row_bytes(tpr, vpl) + na * tpr * 4 + 1024 <= 232448 ? 3 : 2;
+}
+__host__ __device__ constexpr int bwd_ring_bytes(int tpr, int vpl, int na) {
+  return bwd_threads(tpr, na) / tpr * bwd_stages(tpr, vpl, na) * 3 * ring_row_bytes(tpr, vpl);
 }
 template <typename T, int VPL, bool VEC, bool P32>
 __host__ __device__ constexpr bool bwd_param_regs() {
@@ -469,18 +473,17 @@ __host__ __device__ constexpr bool bwd_param_regs() {
 }
 
 template <typename T, int TPR, int VPL, bool VEC, bool P32>
-__global__ void __launch_bounds__(bwd_threads(TPR), 1)
+__global__ void __launch_bounds__(bwd_threads(TPR, VPL * Elem<T>::E), 1)
     ln_bwd_kernel(const LnBackward p) {
   constexpr int E = Elem<T>::E;
-  constexpr int GROUPS = bwd_threads(TPR) / TPR;
   constexpr int NA = VPL * E;  // columns of a thread
+  constexpr int THREADS = bwd_threads(TPR, NA), GROUPS = THREADS / TPR;
   constexpr int RB = ring_row_bytes(TPR, VPL);
-  constexpr int STAGES = bwd_stages(TPR);
+  constexpr int STAGES = bwd_stages(TPR, VPL, NA);
   constexpr bool REGS = bwd_param_regs<T, VPL, VEC, P32>();
   static_assert(TPR >= 32, "a warp shares a row");
   __shared__ float2 red[TPR > 32 ? GROUPS * 2 * (TPR / 32) : 1];
   extern __shared__ __align__(16) uint8_t s_dyn[];
-  float* s_acc = reinterpret_cast<float*>(s_dyn);  // [GROUPS / 2][2][NA][TPR]
   pdl_trigger();
   pdl_wait();
   const int group = threadIdx.x / TPR, l = threadIdx.x % TPR;
@@ -504,7 +507,7 @@ __global__ void __launch_bounds__(bwd_threads(TPR), 1)
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) fetch(row + i * step, i);
   const Params<T, TPR, VPL, VEC, P32, REGS> gamma(
-      p.gamma, 1.f, C, group, l, reinterpret_cast<uint64_t*>(s_dyn + bwd_ring_bytes(TPR, VPL)));
+      p.gamma, 1.f, C, group, l, reinterpret_cast<uint64_t*>(s_dyn + bwd_ring_bytes(TPR, VPL, NA)));
   if constexpr (!REGS) __syncthreads();
   uint64_t dg2[NA / 2], db2[NA / 2];  // pairs of columns
 #pragma unroll
@@ -581,77 +584,56 @@ __global__ void __launch_bounds__(bwd_threads(TPR), 1)
     }
   }
   cp_async_wait<0>();
-  __syncthreads();  // the ring becomes the sums' memory
+  __syncthreads();  // the ring's memory now adds up the sums
   if (p.partials == nullptr) return;
-  float dg[NA], db[NA];
+  // every group's sums to [group][dgamma, dbeta][column], then one thread per column adds the
+  // groups in order
+  constexpr int W = TPR * NA;  // columns with padding
+  float* acc = reinterpret_cast<float*>(s_dyn);
 #pragma unroll
-  for (int k = 0; k < NA / 2; ++k) {
-    const float2 a = f2unpack(dg2[k]), b = f2unpack(db2[k]);
-    dg[2 * k] = a.x;
-    dg[2 * k + 1] = a.y;
-    db[2 * k] = b.x;
-    db[2 * k + 1] = b.y;
-  }
-  // the block's groups added pairwise in shared memory, the upper half into the lower
+  for (int i = 0; i < VPL; ++i) {
+    float4* a = reinterpret_cast<float4*>(acc + group * 2 * W + col_of<T, TPR>(l, i));
 #pragma unroll
-  for (int n = GROUPS; n > 1;) {
-    const int h = (n + 1) / 2;
-    if (group >= h && group < n) {
-      float* a = s_acc + static_cast<size_t>(group - h) * 2 * NA * TPR + l;
-#pragma unroll
-      for (int k = 0; k < NA; ++k) {
-        a[k * TPR] = dg[k];
-        a[(NA + k) * TPR] = db[k];
-      }
+    for (int e = 0; e < E / 4; ++e) {
+      const float2 u = f2unpack(dg2[i * E / 2 + 2 * e]), v = f2unpack(dg2[i * E / 2 + 2 * e + 1]);
+      a[e] = make_float4(u.x, u.y, v.x, v.y);
+      const float2 q = f2unpack(db2[i * E / 2 + 2 * e]), r = f2unpack(db2[i * E / 2 + 2 * e + 1]);
+      a[W / 4 + e] = make_float4(q.x, q.y, r.x, r.y);
     }
-    __syncthreads();
-    if (group + h < n) {
-      const float* a = s_acc + static_cast<size_t>(group) * 2 * NA * TPR + l;
-#pragma unroll
-      for (int k = 0; k < NA; ++k) {
-        dg[k] += a[k * TPR];
-        db[k] += a[(NA + k) * TPR];
-      }
-    }
-    __syncthreads();
-    n = h;
   }
-  if (group == 0) {
-    float* out = p.partials + static_cast<int64_t>(blockIdx.x) * 2 * C;
+  __syncthreads();
+  float* out = p.partials + static_cast<int64_t>(blockIdx.x) * 2 * C;
+  for (int k = threadIdx.x; k < 2 * W; k += THREADS) {
+    const int c = k < W ? k : k - W;
+    if (c < C) {
+      float v = acc[k];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int c = col_of<T, TPR>(l, i) + e;
-        if (c < C) {
-          out[c] = dg[i * E + e];
-          out[C + c] = db[i * E + e];
-        }
-      }
+      for (int g = 1; g < GROUPS; ++g) v += acc[g * 2 * W + k];
+      out[k < W ? c : C + c] = v;
     }
   }
 }
 
 // out[c] = sum of partials[p][c], p = 0 .. P-1, for n columns; columns below `split` go to
-// out0, the others to out1 (either may be null). 32 columns per block, 8 threads per column
-// taking every eighth partial, their sums added in order.
-__global__ void __launch_bounds__(256)
+// out0, the others to out1 (either may be null). 32 columns per block, 16 threads per column
+// taking every sixteenth partial, their sums added in order.
+__global__ void __launch_bounds__(512)
     col_reduce_kernel(const float* partials, int P, int n, int split, float* out0, float* out1) {
-  __shared__ float s[8][32];
+  __shared__ float s[16][32];
   pdl_trigger();
   pdl_wait();
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int c = static_cast<int>(blockIdx.x) * 32 + tx;
   float v = 0.f;
   if (c < n) {
-#pragma unroll 8
-    for (int r = ty; r < P; r += 8) v += partials[static_cast<int64_t>(r) * n + c];
+#pragma unroll 10
+    for (int r = ty; r < P; r += 16) v += partials[static_cast<int64_t>(r) * n + c];
   }
   s[ty][tx] = v;
   __syncthreads();
   if (ty == 0 && c < n) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) v += s[i][tx];
+    for (int i = 1; i < 16; ++i) v += s[i][tx];
     float* out = c < split ? out0 : out1;
     if (out != nullptr) out[c < split ? c : c - split] = v;
   }
@@ -659,7 +641,7 @@ __global__ void __launch_bounds__(256)
 
 cudaError_t launch_col_reduce(const float* partials, int P, int n, int split, float* out0,
                               float* out1, cudaStream_t stream, bool pdl) {
-  return launch(col_reduce_kernel, dim3((n + 31) / 32), dim3(256), 0, stream, pdl, partials, P, n,
+  return launch(col_reduce_kernel, dim3((n + 31) / 32), dim3(512), 0, stream, pdl, partials, P, n,
                 split, out0, out1);
 }
 
@@ -728,11 +710,11 @@ cudaError_t launch_ln_quantize(const LnForward& p, int dtype, int num_sms, cudaS
 }
 
 template <typename T, int TPR, int VPL, bool VEC, bool P32>
-static cudaError_t go_bwd_p(const LnBackward& p, int blocks, cudaStream_t s) {
-  static_assert(bwd_threads(TPR) / TPR / 2 * 2 * VPL * Elem<T>::E * TPR * 4 <= bwd_ring_bytes(TPR, VPL),
-                "the sums fit the ring");
-  constexpr size_t smem = bwd_ring_bytes(TPR, VPL) +
-                          (bwd_param_regs<T, VPL, VEC, P32>() ? 0 : VPL * Elem<T>::E * TPR * 4);
+static cudaError_t go_bwd_p(const LnBackward& p, int num_sms, int* P, cudaStream_t s) {
+  constexpr int NA = VPL * Elem<T>::E, threads = bwd_threads(TPR, NA);
+  static_assert(threads * NA * 8 <= bwd_ring_bytes(TPR, VPL, NA), "the sums fit the ring");
+  constexpr size_t smem =
+      bwd_ring_bytes(TPR, VPL, NA) + (bwd_param_regs<T, VPL, VEC, P32>() ? 0 : NA * TPR * 4);
   static_assert(smem + 1024 <= 232448, "shared memory");
   auto kern = ln_bwd_kernel<T, TPR, VPL, VEC, P32>;
   if constexpr (smem > 40 * 1024) {  // with the static part past the default 48 KB
@@ -740,49 +722,45 @@ static cudaError_t go_bwd_p(const LnBackward& p, int blocks, cudaStream_t s) {
                                                static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  return launch(kern, dim3(blocks), dim3(bwd_threads(TPR)), smem, s, false, p);
+  const int64_t blocks = (static_cast<int64_t>(p.M) + threads / TPR - 1) / (threads / TPR);
+  *P = static_cast<int>(blocks < num_sms ? blocks : num_sms);
+  return launch(kern, dim3(*P), dim3(threads), smem, s, false, p);
 }
 template <typename T, int TPR, int VPL, bool VEC>
-static cudaError_t go_bwd(const LnBackward& p, int blocks, cudaStream_t s) {
-  if constexpr (sizeof(T) == 4) return go_bwd_p<T, TPR, VPL, VEC, true>(p, blocks, s);
-  return p.p32 ? go_bwd_p<T, TPR, VPL, VEC, true>(p, blocks, s)
-               : go_bwd_p<T, TPR, VPL, VEC, false>(p, blocks, s);
+static cudaError_t go_bwd(const LnBackward& p, int num_sms, int* P, cudaStream_t s) {
+  if constexpr (sizeof(T) == 4) return go_bwd_p<T, TPR, VPL, VEC, true>(p, num_sms, P, s);
+  return p.p32 ? go_bwd_p<T, TPR, VPL, VEC, true>(p, num_sms, P, s)
+               : go_bwd_p<T, TPR, VPL, VEC, false>(p, num_sms, P, s);
 }
 
-// Threads per row and vectors per thread, by the row's 16-byte vectors: at most 4 vectors a
-// thread, so that its columns' sums and two rows of three tensors stay in registers.
+// Threads per row and vectors per thread, by the row's 16-byte vectors: at most 24 columns of
+// 16-bit values a thread (at 32, its sums and rows spill: 50000 x 1024 bf16 97 us against 75
+// with 64 threads of 16 columns), 16 of fp32. *P is the number of blocks, each with a partial.
 template <typename T, bool VEC>
-static cudaError_t pick_bwd(const LnBackward& p, int blocks, cudaStream_t s) {
+static cudaError_t pick_bwd(const LnBackward& p, int num_sms, int* P, cudaStream_t s) {
   const int n = (p.C + Elem<T>::E - 1) / Elem<T>::E;
-  if (n <= 32) return go_bwd<T, 32, 1, VEC>(p, blocks, s);
-  if (n <= 64) return go_bwd<T, 32, 2, VEC>(p, blocks, s);
-  if (n <= 96) return go_bwd<T, 32, 3, VEC>(p, blocks, s);
-  if (n <= 128) return go_bwd<T, 32, 4, VEC>(p, blocks, s);
-  if (n <= 256) return go_bwd<T, 64, 4, VEC>(p, blocks, s);
-  if (n <= 512) return go_bwd<T, 128, 4, VEC>(p, blocks, s);
-  if (n <= 1024) return go_bwd<T, 256, 4, VEC>(p, blocks, s);
-  if constexpr (sizeof(T) == 4) return go_bwd<T, 512, 4, VEC>(p, blocks, s);
+  if (n <= 32) return go_bwd<T, 32, 1, VEC>(p, num_sms, P, s);
+  if (n <= 64) return go_bwd<T, 32, 2, VEC>(p, num_sms, P, s);
+  if (n <= 96) return go_bwd<T, 32, 3, VEC>(p, num_sms, P, s);
+  if (n <= 128) return go_bwd<T, 64, 2, VEC>(p, num_sms, P, s);
+  if (n <= 192) return go_bwd<T, 64, 3, VEC>(p, num_sms, P, s);
+  if (n <= 256) return go_bwd<T, 128, 2, VEC>(p, num_sms, P, s);
+  if (n <= 512) return go_bwd<T, 256, 2, VEC>(p, num_sms, P, s);
+  if (n <= 1024) return go_bwd<T, 512, 2, VEC>(p, num_sms, P, s);
+  if constexpr (sizeof(T) == 4) return go_bwd<T, 512, 4, VEC>(p, num_sms, P, s);
   return cudaErrorInvalidValue;
-}
-
-// Blocks of the backward kernel: one per SM, or fewer when the rows run out.
-static int bwd_blocks(int M, int C, int elem, int num_sms) {
-  const int n = (C + elem - 1) / elem;
-  const int rows = n <= 128 ? 12 : n <= 256 ? 6 : n <= 512 ? 3 : 1;  // per block and step
-  const int64_t blocks = (static_cast<int64_t>(M) + rows - 1) / rows;
-  return static_cast<int>(blocks < num_sms ? blocks : num_sms);
 }
 
 cudaError_t launch_ln_backward(const LnBackward& p, int dtype, bool vec, int num_sms, float* dgamma,
                                float* dbeta, cudaStream_t s) {
-  const int blocks = bwd_blocks(p.M, p.C, dtype == RS_FP32 ? 4 : 8, num_sms);
+  int blocks = 0;
   cudaError_t e;
   if (dtype == RS_BF16)
-    e = vec ? pick_bwd<__nv_bfloat16, true>(p, blocks, s) : pick_bwd<__nv_bfloat16, false>(p, blocks, s);
+    e = vec ? pick_bwd<__nv_bfloat16, true>(p, num_sms, &blocks, s) : pick_bwd<__nv_bfloat16, false>(p, num_sms, &blocks, s);
   else if (dtype == RS_FP16)
-    e = vec ? pick_bwd<__half, true>(p, blocks, s) : pick_bwd<__half, false>(p, blocks, s);
+    e = vec ? pick_bwd<__half, true>(p, num_sms, &blocks, s) : pick_bwd<__half, false>(p, num_sms, &blocks, s);
   else
-    e = vec ? pick_bwd<float, true>(p, blocks, s) : pick_bwd<float, false>(p, blocks, s);
+    e = vec ? pick_bwd<float, true>(p, num_sms, &blocks, s) : pick_bwd<float, false>(p, num_sms, &blocks, s);
   if (e != cudaSuccess || p.partials == nullptr) return e;
   return launch_col_reduce(p.partials, blocks, 2 * p.C, p.C, dgamma, dbeta, s, true);
 }
