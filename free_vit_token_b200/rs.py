@@ -8,6 +8,7 @@ a missing library is an error.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional, Tuple
 
@@ -128,9 +129,14 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return t.data_ptr() or None
 
 
+# The current stream's handle without building a torch.cuda.Stream object (3 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream or None
+        return _raw_stream(torch.cuda.current_device()) or None
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream or None
     return int(stream) or None
@@ -510,54 +516,62 @@ class Fp8(NamedTuple):
     K: int
 
 
-def _rows(t: torch.Tensor, name: str, width: Optional[int] = None,
-          dtype: Optional[torch.dtype] = None, rows: Optional[int] = None) -> Tuple[int, int, int]:
+def _device(t: torch.Tensor, name: str) -> int:
+    """The index of the current CUDA device, which `t` must be on."""
+    d = t.get_device()
+    if d < 0 or d != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    return d
+
+
+def _rows(t: torch.Tensor, name: str, dev: int, dtype: Optional[torch.dtype] = None,
+          width: Optional[int] = None, rows: Optional[int] = None) -> Tuple[Optional[int], int, int]:
     """(address, row stride, rows) of a matrix whose rows may be strided; tensors of more
     dimensions count as their rows and must be contiguous."""
-    if t.dim() == 2:
-        n, w = t.shape
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{name}: {dtype} wanted, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current CUDA device")
+    shape = t.shape
+    if t.is_contiguous():
+        if len(shape) == 0:
+            raise ValueError(f"{name} must be a matrix or a contiguous tensor")
+        w = ld = shape[-1]
+        n = shape[0] if len(shape) == 2 else t.numel() // max(w, 1)
+    else:
+        if len(shape) != 2:
+            raise ValueError(f"{name} must be a matrix or a contiguous tensor")
+        n, w = shape
         ld, step = t.stride()
         if w > 1 and step != 1:
             raise ValueError(f"{name}: the elements of a row must be contiguous")
-        if n < 2 or w == 0:
-            ld = max(ld, w, 1) if n else max(w, 1)
-    else:
-        if not t.is_contiguous() or t.dim() == 0:
-            raise ValueError(f"{name} must be a matrix or a contiguous tensor")
-        w = t.shape[-1]
-        n, ld = t.numel() // max(w, 1), w
-    if ld < w:
-        raise ValueError(f"{name}: rows overlap")
+        if n > 1 and ld < w:
+            raise ValueError(f"{name}: rows overlap")
+        ld = max(ld, w)
     if width is not None and w != width:
         raise ValueError(f"{name}: rows of {width} wanted, got {w}")
     if rows is not None and n != rows:
         raise ValueError(f"{name}: {rows} rows wanted, got {n}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name}: {dtype} wanted, got {t.dtype}")
-    _on_device(t, name)
     return t.data_ptr() or None, ld, n
 
 
-def _on_device(t: torch.Tensor, name: str) -> None:
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current CUDA device")
-
-
-def _vec(t: Optional[torch.Tensor], name: str, n: int, dtype: torch.dtype) -> Optional[int]:
-    """Address of a contiguous vector of n elements (None for None)."""
+def _vec(t: Optional[torch.Tensor], name: str, dev: int, n: int,
+         dtype: torch.dtype) -> Optional[int]:
+    """Address of a contiguous tensor of n elements (None for None)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} tensor of {n} elements wanted")
-    _on_device(t, name)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current CUDA device")
     return t.data_ptr() or None
 
 
-def _params(x: torch.Tensor, C: int, gamma, beta) -> Tuple[int, Optional[int], Optional[int]]:
+def _params(x: torch.Tensor, dev: int, C: int, gamma, beta):
     dt = gamma.dtype if gamma is not None else beta.dtype if beta is not None else x.dtype
-    if dt != torch.float32 and dt != x.dtype:
+    if dt is not torch.float32 and dt is not x.dtype:
         raise ValueError("gamma and beta must be float32 or of x's type")
-    return _DTYPES[dt], _vec(gamma, "gamma", C, dt), _vec(beta, "beta", C, dt)
+    return _DTYPES[dt], _vec(gamma, "gamma", dev, C, dt), _vec(beta, "beta", dev, C, dt)
 
 
 def _float_type(x: torch.Tensor) -> int:
@@ -566,34 +580,60 @@ def _float_type(x: torch.Tensor) -> int:
     return _DTYPES[x.dtype]
 
 
-def _ws(n: int, dev, ws: Optional[torch.Tensor]) -> Tuple[Optional[int], int, Optional[torch.Tensor]]:
-    """The caller's scratch tensor, or one of n bytes from torch's allocator (the tensor is
-    returned too: it must live until the call is queued)."""
+@functools.lru_cache(maxsize=4096)
+def _ws_size(name: str, *sizes: int) -> int:
+    return int(getattr(lib(), name)(*sizes))
+
+
+def _ws(ws: Optional[torch.Tensor], device: torch.device, dev: int, name: str, *sizes: int):
+    """(address, bytes, tensor) of the caller's scratch, or of scratch from torch's allocator
+    (the tensor must live until the call is queued). `name` is the size function."""
     if ws is None:
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    else:
-        if not ws.is_contiguous():
-            raise ValueError("ws must be contiguous")
-        _on_device(ws, "ws")
+        n = _ws_size(name, *sizes)
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        return ws.data_ptr() or None, n, ws
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    if ws.get_device() != dev:
+        raise ValueError("ws must be on the current CUDA device")
     return ws.data_ptr() or None, ws.numel() * ws.element_size(), ws
 
 
-def _fp8_empty(rows: int, K: int, dev) -> Fp8:
-    q = torch.empty(rows, (K + 15) // 16 * 16, dtype=torch.float8_e4m3fn, device=dev)
-    n = (rows + 127) // 128 * ((K + 511) // 512) * 512
-    return Fp8(q, torch.empty(n, dtype=torch.uint8, device=dev), rows, K)
+def _like(x: torch.Tensor) -> torch.Tensor:
+    """An uninitialised contiguous tensor of x's shape and type."""
+    if x.is_contiguous():
+        return torch.empty_like(x)
+    return torch.empty(*x.shape, dtype=x.dtype, device=x.device)
 
 
-def _fp8(t: Fp8, name: str, rows: Optional[int] = None, K: Optional[int] = None):
+def _matrix(x: torch.Tensor, M: int, N: int, dtype: torch.dtype) -> torch.Tensor:
+    """An uninitialised tensor with x's leading dimensions (M rows in all) and N columns."""
+    if x.dim() == 2:
+        return torch.empty(M, N, dtype=dtype, device=x.device)
+    return torch.empty(*x.shape[:-1], N, dtype=dtype, device=x.device)
+
+
+def _scale_bytes(rows: int, K: int) -> int:
+    return (rows + 127) // 128 * ((K + 511) // 512) * 512
+
+
+def _fp8_empty(rows: int, K: int, device) -> Fp8:
+    return Fp8(torch.empty(rows, (K + 15) // 16 * 16, dtype=torch.float8_e4m3fn, device=device),
+               torch.empty(_scale_bytes(rows, K), dtype=torch.uint8, device=device), rows, K)
+
+
+def _fp8(t: Fp8, name: str, dev: int, rows: Optional[int] = None, K: Optional[int] = None):
     """(q address, row stride, scales address) of a quantised operand."""
-    if (rows is not None and t.rows != rows) or (K is not None and t.K != K):
-        raise ValueError(f"{name}: [{rows}, {K}] wanted, got [{t.rows}, {t.K}]")
-    q, ld, _ = _rows(t.q, name, dtype=torch.float8_e4m3fn, rows=t.rows)
-    if t.q.shape[-1] < t.K:
+    q, s, r, k = t
+    if (rows is not None and r != rows) or (K is not None and k != K):
+        raise ValueError(f"{name}: [{rows}, {K}] wanted, got [{r}, {k}]")
+    pq, ld, _ = _rows(q, name, dev, torch.float8_e4m3fn, rows=r)
+    if q.shape[-1] < k:
         raise ValueError(f"{name}: rows shorter than K")
-    if t.scales.numel() < (t.rows + 127) // 128 * ((t.K + 511) // 512) * 512:
+    n = s.numel()
+    if n < _scale_bytes(r, k):
         raise ValueError(f"{name}: too few scale bytes")
-    return q, ld, _vec(t.scales, f"{name} scales", t.scales.numel(), torch.uint8)
+    return pq, ld, _vec(s, f"{name} scales", dev, n, torch.uint8)
 
 
 def rs_ln_forward(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
@@ -601,18 +641,22 @@ def rs_ln_forward(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
                   y: Optional[torch.Tensor] = None, stats: Optional[torch.Tensor] = None,
                   stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """x [..., C] (bf16, fp16 or fp32; a matrix may have strided rows) -> (LN(x) of the same
-    type, stats [M, 2] fp32 with each row's mean and 1/std for rs_ln_backward)."""
-    dt = _float_type(x)
+    type, stats [M, 2] fp32 with each row's mean and 1/std for rs_ln_backward). y may be x."""
+    dev, dt = _device(x, "x"), _float_type(x)
+    px, ldx, M = _rows(x, "x", dev)
     C = x.shape[-1]
-    px, ldx, M = _rows(x, "x")
-    pdt, pg, pb = _params(x, C, gamma, beta)
+    pdt, pg, pb = _params(x, dev, C, gamma, beta)
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = _like(x)
+        py, ldy = y.data_ptr() or None, C
+    else:
+        py, ldy, _ = _rows(y, "y", dev, x.dtype, C, M)
     if stats is None:
         stats = torch.empty(M, 2, dtype=torch.float32, device=x.device)
-    py, ldy, _ = _rows(y, "y", C, x.dtype, M)
-    _check(lib().rs_ln_forward(px, ldx, M, C, dt, pg, pb, pdt, eps, py, ldy,
-                               _vec(stats, "stats", 2 * M, torch.float32), _stream(stream)),
+        ps = stats.data_ptr() or None
+    else:
+        ps = _vec(stats, "stats", dev, 2 * M, torch.float32)
+    _check(lib().rs_ln_forward(px, ldx, M, C, dt, pg, pb, pdt, eps, py, ldy, ps, _stream(stream)),
            "rs_ln_forward")
     return y, stats
 
@@ -623,15 +667,15 @@ def rs_ln_quantize(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
                    stream=None) -> Fp8:
     """LN(x) in 8-bit blocks along C (x bf16 or fp16, C a multiple of 8); `stats` [M, 2] fp32
     also receives each row's mean and 1/std."""
-    dt = _float_type(x)
+    dev, dt = _device(x, "x"), _float_type(x)
+    px, ldx, M = _rows(x, "x", dev)
     C = x.shape[-1]
-    px, ldx, M = _rows(x, "x")
-    pdt, pg, pb = _params(x, C, gamma, beta)
+    pdt, pg, pb = _params(x, dev, C, gamma, beta)
     if out is None:
         out = _fp8_empty(M, C, x.device)
-    q, ldq, sc = _fp8(out, "out", M, C)
+    q, ldq, sc = _fp8(out, "out", dev, M, C)
     _check(lib().rs_ln_quantize(px, ldx, M, C, dt, pg, pb, pdt, eps, q, ldq, sc,
-                                _vec(stats, "stats", 2 * M, torch.float32), _stream(stream)),
+                                _vec(stats, "stats", dev, 2 * M, torch.float32), _stream(stream)),
            "rs_ln_quantize")
     return out
 
@@ -643,26 +687,25 @@ def rs_ln_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor,
                    stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """Gradients of y = LN(x) for dy: (dx, of x's type, with `dres` added; dgamma [C] fp32;
     dbeta [C] fp32). `stats` as rs_ln_forward returned them; dx may be dres."""
-    dt = _float_type(x)
-    C = x.shape[-1]
-    px, ldx, M = _rows(x, "x")
-    pdy, lddy, _ = _rows(dy, "dy", C, x.dtype, M)
-    pdr, lddr = (None, C) if dres is None else _rows(dres, "dres", C, x.dtype, M)[:2]
-    pdt, pg, _ = _params(x, C, gamma, None)
-    dev = x.device
+    dev, dt = _device(x, "x"), _float_type(x)
+    px, ldx, M = _rows(x, "x", dev)
+    C, device, f32 = x.shape[-1], x.device, torch.float32
+    pdy, lddy, _ = _rows(dy, "dy", dev, x.dtype, C, M)
+    pdr, lddr = (None, C) if dres is None else _rows(dres, "dres", dev, x.dtype, C, M)[:2]
+    pdt, pg, _ = _params(x, dev, C, gamma, None)
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        dx = _like(x)
+        pdx, lddx = dx.data_ptr() or None, C
+    else:
+        pdx, lddx, _ = _rows(dx, "dx", dev, x.dtype, C, M)
     if dgamma is None:
-        dgamma = torch.empty(C, dtype=torch.float32, device=dev)
+        dgamma = torch.empty(C, dtype=f32, device=device)
     if dbeta is None:
-        dbeta = torch.empty(C, dtype=torch.float32, device=dev)
-    pdx, lddx, _ = _rows(dx, "dx", C, x.dtype, M)
-    n = 0 if ws is not None else lib().rs_ln_backward_ws_bytes(M, C)
-    pw, nw, ws = _ws(n, dev, ws)
-    st = lib().rs_ln_backward(pdy, lddy, px, ldx, pdr, lddr,
-                              _vec(stats, "stats", 2 * M, torch.float32), pg, pdt, M, C, dt, pdx,
-                              lddx, _vec(dgamma, "dgamma", C, torch.float32),
-                              _vec(dbeta, "dbeta", C, torch.float32), pw, nw, _stream(stream))
+        dbeta = torch.empty(C, dtype=f32, device=device)
+    pw, nw, ws = _ws(ws, device, dev, "rs_ln_backward_ws_bytes", M, C)
+    st = lib().rs_ln_backward(pdy, lddy, px, ldx, pdr, lddr, _vec(stats, "stats", dev, 2 * M, f32),
+                              pg, pdt, M, C, dt, pdx, lddx, _vec(dgamma, "dgamma", dev, C, f32),
+                              _vec(dbeta, "dbeta", dev, C, f32), pw, nw, _stream(stream))
     _check(st, "rs_ln_backward")
     return dx, dgamma, dbeta
 
@@ -677,24 +720,26 @@ def rs_fp8_quantize(x: torch.Tensor, rows: bool = True, cols: bool = False, cols
     """x [M, K] (bf16, fp16 or fp32) to 8-bit blocks of 128 along K (`rows`), and/or its
     transpose [K, M] in blocks along M (`cols`), and/or its column sums [K] fp32 (`colsum`,
     needs cols), from one read: a triple, None for what was not asked for."""
-    dt = _float_type(x)
-    K = x.shape[-1]
-    px, ldx, M = _rows(x, "x")
-    dev = x.device
+    dev, dt = _device(x, "x"), _float_type(x)
+    px, ldx, M = _rows(x, "x", dev)
+    K, device = x.shape[-1], x.device
     if colsum and not cols:
         raise ValueError("colsum needs cols")
-    if rows and out is None:
-        out = _fp8_empty(M, K, dev)
-    if cols and out_t is None:
-        out_t = _fp8_empty(K, M, dev)
-    q, ldq, sc = _fp8(out, "out", M, K) if rows else (None, 0, None)
-    qt, ldqt, sct = _fp8(out_t, "out_t", K, M) if cols else (None, 0, None)
-    sums, ws, pw, nw = None, None, None, 0
+    q = qt = sc = sct = sums = ws = pw = ps = None
+    ldq = ldqt = nw = 0
+    if rows:
+        if out is None:
+            out = _fp8_empty(M, K, device)
+        q, ldq, sc = _fp8(out, "out", dev, M, K)
+    if cols:
+        if out_t is None:
+            out_t = _fp8_empty(K, M, device)
+        qt, ldqt, sct = _fp8(out_t, "out_t", dev, K, M)
     if colsum:
-        sums = torch.empty(K, dtype=torch.float32, device=dev)
-        pw, nw, ws = _ws(lib().rs_fp8_quantize_ws_bytes(M, K), dev, None)
-    _check(lib().rs_fp8_quantize(px, ldx, M, K, dt, q, ldq, sc, qt, ldqt, sct,
-                                 None if sums is None else sums.data_ptr(), pw, nw,
+        sums = torch.empty(K, dtype=torch.float32, device=device)
+        ps = sums.data_ptr()
+        pw, nw, ws = _ws(None, device, dev, "rs_fp8_quantize_ws_bytes", M, K)
+    _check(lib().rs_fp8_quantize(px, ldx, M, K, dt, q, ldq, sc, qt, ldqt, sct, ps, pw, nw,
                                  _stream(stream)), "rs_fp8_quantize")
     return out if rows else None, out_t if cols else None, sums
 
@@ -704,28 +749,31 @@ def rs_fp8_gemm(a: Fp8, b: Fp8, bias: Optional[torch.Tensor] = None, gelu: bool 
                 out_dtype: Optional[torch.dtype] = None, stream=None):
     """act(A B^T + bias) + resid of two quantised operands [M, K] and [N, K]: a bf16 (default)
     or fp32 tensor [M, N], or with out_dtype=torch.float8_e4m3fn an Fp8."""
-    M, N, K = a.rows, b.rows, a.K
-    pa, lda, sa = _fp8(a, "a")
-    pb, ldb, sb = _fp8(b, "b", K=K)
+    M, N, K, device = a.rows, b.rows, a.K, a.q.device
+    dev = _device(a.q, "a")
+    pa, lda, sa = _fp8(a, "a", dev)
+    pb, ldb, sb = _fp8(b, "b", dev, K=K)
     if out_dtype is None:
         out_dtype = (torch.bfloat16 if out is None else
                      torch.float8_e4m3fn if isinstance(out, Fp8) else out.dtype)
-    if out_dtype == torch.float8_e4m3fn:
+    so, pr, ldr = None, None, N
+    if out_dtype is torch.float8_e4m3fn:
         if out is None:
-            out = _fp8_empty(M, N, a.q.device)
-        po, ldo, so = _fp8(out, "out", M, N)
+            out = _fp8_empty(M, N, device)
+        po, ldo, so = _fp8(out, "out", dev, M, N)
         dt = RS_E4M3
     else:
-        if out_dtype not in (torch.bfloat16, torch.float32):
+        if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
             raise ValueError("out_dtype: bfloat16, float32 or float8_e4m3fn")
         if out is None:
-            out = torch.empty(M, N, dtype=out_dtype, device=a.q.device)
-        po, ldo, _ = _rows(out, "out", N, out_dtype, M)
-        so, dt = None, _DTYPES[out_dtype]
-    pr, ldr = (None, N) if resid is None else _rows(resid, "resid", N, out_dtype, M)[:2]
+            out = torch.empty(M, N, dtype=out_dtype, device=device)
+        po, ldo, _ = _rows(out, "out", dev, out_dtype, N, M)
+        dt = _DTYPES[out_dtype]
+    if resid is not None:
+        pr, ldr, _ = _rows(resid, "resid", dev, out_dtype, N, M)
     _check(lib().rs_fp8_gemm(pa, lda, sa, pb, ldb, sb, M, N, K,
-                             _vec(bias, "bias", N, torch.bfloat16), int(gelu), pr, ldr, po, ldo,
-                             dt, so, _stream(stream)), "rs_fp8_gemm")
+                             _vec(bias, "bias", dev, N, torch.bfloat16), int(gelu), pr, ldr, po,
+                             ldo, dt, so, _stream(stream)), "rs_fp8_gemm")
     return out
 
 
@@ -735,18 +783,20 @@ def rs_fp8_linear(x: torch.Tensor, w: Fp8, bias: Optional[torch.Tensor] = None,
                   stream=None) -> torch.Tensor:
     """x [..., K] bf16, quantised along K in the call, through a linear layer whose weight
     [N, K] is held in 8 bits: act(x W^T + bias) + resid [..., N] bf16."""
-    N, K = w.rows, w.K
-    px, ldx, M = _rows(x, "x", K, torch.bfloat16)
-    pw, ldw, sw = _fp8(w, "w")
+    N, K, bf = w.rows, w.K, torch.bfloat16
+    dev = _device(x, "x")
+    px, ldx, M = _rows(x, "x", dev, bf, K)
+    pw, ldw, sw = _fp8(w, "w", dev)
     if out is None:
-        out = torch.empty(*x.shape[:-1], N, dtype=torch.bfloat16, device=x.device)
-    po, ldo, _ = _rows(out, "out", N, torch.bfloat16, M)
-    pr, ldr = (None, N) if resid is None else _rows(resid, "resid", N, torch.bfloat16, M)[:2]
-    n = 0 if ws is not None else lib().rs_fp8_linear_ws_bytes(M, K)
-    pws, nws, ws = _ws(n, x.device, ws)
-    _check(lib().rs_fp8_linear(px, ldx, M, K, N, pw, ldw, sw,
-                               _vec(bias, "bias", N, torch.bfloat16), int(gelu), pr, ldr, po, ldo,
-                               pws, nws, _stream(stream)), "rs_fp8_linear")
+        out = _matrix(x, M, N, bf)
+        po, ldo = out.data_ptr() or None, N
+    else:
+        po, ldo, _ = _rows(out, "out", dev, bf, N, M)
+    pr, ldr = (None, N) if resid is None else _rows(resid, "resid", dev, bf, N, M)[:2]
+    pws, nws, ws = _ws(ws, x.device, dev, "rs_fp8_linear_ws_bytes", M, K)
+    _check(lib().rs_fp8_linear(px, ldx, M, K, N, pw, ldw, sw, _vec(bias, "bias", dev, N, bf),
+                               int(gelu), pr, ldr, po, ldo, pws, nws, _stream(stream)),
+           "rs_fp8_linear")
     return out
 
 
@@ -757,26 +807,31 @@ def rs_fp8_linear_backward(dy: torch.Tensor, xt: Optional[Fp8], wt: Optional[Fp8
     operands (rs_fp8_quantize(..., cols=True)): xt of x, [K, M], and wt of W, [K, N]. Returns
     (dx [M, K] bf16, dw [N, K], db [N] fp32), None for dx without wt, dw without xt and db
     without `bias`."""
-    N = dy.shape[-1]
-    pdy, lddy, M = _rows(dy, "dy", dtype=torch.bfloat16)
+    dev = _device(dy, "dy")
+    pdy, lddy, M = _rows(dy, "dy", dev, torch.bfloat16)
+    N, device = dy.shape[-1], dy.device
     if xt is None and wt is None:
         raise ValueError("xt or wt wanted")
-    K = xt.rows if xt is not None else wt.rows
-    dev = dy.device
-    px, ldx, sx = _fp8(xt, "xt", K, M) if xt is not None else (None, 0, None)
-    pw, ldw, sw = _fp8(wt, "wt", K, N) if wt is not None else (None, 0, None)
-    if dw_dtype not in (torch.bfloat16, torch.float32):
+    if dw_dtype is not torch.bfloat16 and dw_dtype is not torch.float32:
         raise ValueError("dw_dtype: bfloat16 or float32")
-    dx = torch.empty(*dy.shape[:-1], K, dtype=torch.bfloat16, device=dev) if wt is not None else None
-    dw = torch.empty(N, K, dtype=dw_dtype, device=dev) if xt is not None else None
-    db = torch.empty(N, dtype=torch.float32, device=dev) if bias else None
-    n = 0 if ws is not None else lib().rs_fp8_linear_backward_ws_bytes(M, N)
-    pws, nws, ws = _ws(n, dev, ws)
-    _check(lib().rs_fp8_linear_backward(pdy, lddy, M, N, K, px, ldx, sx, pw, ldw, sw,
-                                        None if dx is None else dx.data_ptr() or None, K,
-                                        None if dw is None else dw.data_ptr(), K,
-                                        _DTYPES[dw_dtype], None if db is None else db.data_ptr(),
-                                        pws, nws, _stream(stream)), "rs_fp8_linear_backward")
+    K = xt.rows if xt is not None else wt.rows
+    px = sx = pw = sw = dx = dw = db = pdx = pdw = pdb = None
+    ldx = ldw = 0
+    if wt is not None:
+        pw, ldw, sw = _fp8(wt, "wt", dev, K, N)
+        dx = _matrix(dy, M, K, torch.bfloat16)
+        pdx = dx.data_ptr() or None
+    if xt is not None:
+        px, ldx, sx = _fp8(xt, "xt", dev, K, M)
+        dw = torch.empty(N, K, dtype=dw_dtype, device=device)
+        pdw = dw.data_ptr()
+    if bias:
+        db = torch.empty(N, dtype=torch.float32, device=device)
+        pdb = db.data_ptr()
+    pws, nws, ws = _ws(ws, device, dev, "rs_fp8_linear_backward_ws_bytes", M, N)
+    _check(lib().rs_fp8_linear_backward(pdy, lddy, M, N, K, px, ldx, sx, pw, ldw, sw, pdx, K, pdw,
+                                        K, _DTYPES[dw_dtype], pdb, pws, nws, _stream(stream)),
+           "rs_fp8_linear_backward")
     return dx, dw, db
 
 
@@ -784,23 +839,22 @@ def rs_mlp_forward_fp8(x: torch.Tensor, w1: Fp8, b1, w2: Fp8, b2, gamma, beta,
                        out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
                        stream=None) -> torch.Tensor:
     """rs_mlp_forward with W1 [H, C] and W2 [C, H] held in 8-bit blocks and both products in 8
-    bits: x [..., C] bf16 -> x + MLP(LN(x)), same shape."""
-    C, H = w1.K, w1.rows
-    px, ldx, M = _rows(x, "x", C, torch.bfloat16)
+    bits: x [..., C] bf16 -> x + MLP(LN(x)), same shape. out may be x."""
+    C, H, bf = w1.K, w1.rows, torch.bfloat16
+    dev = _device(x, "x")
+    px, ldx, M = _rows(x, "x", dev, bf, C)
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
-    p1, ld1, s1 = _fp8(w1, "w1")
-    p2, ld2, s2 = _fp8(w2, "w2", C, H)
+    p1, ld1, s1 = _fp8(w1, "w1", dev)
+    p2, ld2, s2 = _fp8(w2, "w2", dev, C, H)
     if out is None:
         out = torch.empty_like(x)
     elif not out.is_contiguous():
         raise ValueError("out must be contiguous")
-    bf = torch.bfloat16
-    n = 0 if ws is not None else lib().rs_mlp_forward_fp8_ws_bytes(M, C, H)
-    pws, nws, ws = _ws(n, x.device, ws)
-    st = lib().rs_mlp_forward_fp8(px, M, C, H, p1, ld1, s1, _vec(b1, "b1", H, bf), p2, ld2, s2,
-                                  _vec(b2, "b2", C, bf), _vec(gamma, "gamma", C, bf),
-                                  _vec(beta, "beta", C, bf), _rows(out, "out", C, bf, M)[0], pws,
-                                  nws, _stream(stream))
+    pws, nws, ws = _ws(ws, x.device, dev, "rs_mlp_forward_fp8_ws_bytes", M, C, H)
+    st = lib().rs_mlp_forward_fp8(px, M, C, H, p1, ld1, s1, _vec(b1, "b1", dev, H, bf), p2, ld2, s2,
+                                  _vec(b2, "b2", dev, C, bf), _vec(gamma, "gamma", dev, C, bf),
+                                  _vec(beta, "beta", dev, C, bf),
+                                  _rows(out, "out", dev, bf, C, M)[0], pws, nws, _stream(stream))
     _check(st, "rs_mlp_forward_fp8")
     return out

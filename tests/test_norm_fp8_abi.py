@@ -146,13 +146,24 @@ def test_python_refusals_need_no_gpu():
     import torch
 
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
-    with pytest.raises(ValueError, match="CUDA device|must be on"):
-        rs._on_device(x, "x")
+    cpu = x.get_device()
+    with pytest.raises(ValueError, match="CUDA device"):
+        rs._device(x, "x")
+    with pytest.raises(ValueError, match="CUDA device"):
+        rs._rows(x, "x", 0)
     with pytest.raises(ValueError, match="contiguous"):
-        rs._rows(x.t(), "x")
+        rs._rows(x.t(), "x", cpu)
     with pytest.raises(ValueError, match="rows overlap"):
-        rs._rows(x.as_strided((4, 64), (32, 1)), "x")
+        rs._rows(x.as_strided((2, 64), (32, 1)), "x", cpu)
+    with pytest.raises(ValueError, match="wanted"):
+        rs._rows(x, "x", cpu, torch.float32)
+    with pytest.raises(ValueError, match="rows of 63"):
+        rs._rows(x, "x", cpu, width=63)
+    with pytest.raises(ValueError, match="matrix"):
+        rs._rows(x.view(2, 2, 64)[:, :, :32], "x", cpu)
+    assert rs._rows(x[:, 8:40], "x", cpu)[1:] == (64, 4)
+    assert rs._rows(x[:1, 8:40], "x", cpu)[1] >= 32
     with pytest.raises(ValueError):
         rs._float_type(torch.zeros(2, dtype=torch.float64))
     with pytest.raises(ValueError):
-        rs._params(x, 64, torch.zeros(64, dtype=torch.float16), None)
+        rs._params(x, cpu, 64, torch.zeros(64, dtype=torch.float16), None)
