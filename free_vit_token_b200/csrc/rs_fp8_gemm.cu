@@ -11,10 +11,13 @@
 // before the MMAs that read them; two sets of TMEM columns take turns.
 //
 // One persistent CTA per SM (or a CTA pair with 256-row tiles) loops over 128 x BN tiles:
-//   warps 0-7  epilogue: a tile's accumulator goes to registers at once (up to 128 columns a
+//   warps 0-15 epilogue: a tile's accumulator goes to registers at once (up to 64 columns a
 //              thread) and is handed back, then bias, activation, residual and rounding, and
 //              out through per-warp TMA-store boxes
-//   warp 8     TMA producer, warp 9 TMEM owner and MMA issuer
+//   warp 16    TMA producer, warp 17 TMEM owner and MMA issuer
+// At 8 bits a tile's products take half the time they take in bf16 while its epilogue stays the
+// same: sixteen epilogue warps, not eight, keep up with reductions down to K = 384
+// (50432 x 384 -> 1536 with GELU: 110 us with eight).
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -31,27 +34,24 @@ namespace {
 constexpr int kGM = 128;                       // rows of A per CTA and tile
 constexpr int kGK = 128;                       // K elements (bytes) per stage
 constexpr int kGABytes = kGM * kGK;            // 16 KB
-constexpr int kGEpiWarps = 8;
+constexpr int kGEpiWarps = 16;
+constexpr int kGProducer = kGEpiWarps, kGIssuer = kGEpiWarps + 1;  // warps
 constexpr int kGThreads = (kGEpiWarps + 2) * 32;
 constexpr int kGSmemLimit = 232448;
 constexpr int kGCtrl = 512;
 constexpr int kGBoxBytes = 32 * 64;            // 32 rows of 64 bytes, 64-byte swizzle
-constexpr int kGBoxes = 2;                     // per warp
+constexpr int kGEpiBytes = kGEpiWarps * (kGBoxBytes + 128 + 512);  // boxes, biases, maxima
 
 __host__ __device__ constexpr int g_scale_tiles_b(int bn) { return bn > 128 ? 2 : 1; }
 __host__ __device__ constexpr int g_stage_bytes(int bn, bool pair) {
   return kGABytes + (pair ? bn / 2 : bn) * kGK + (1 + g_scale_tiles_b(bn)) * kScaleTile;
 }
-__host__ __device__ constexpr int g_fixed(int) {
-  return 1024 + kGCtrl + kGEpiWarps * kGBoxes * kGBoxBytes;
-}
+constexpr int kGFixed = 1024 + kGCtrl + kGEpiBytes;
 __host__ __device__ constexpr int g_stages(int bn, bool pair) {
-  return (kGSmemLimit - g_fixed(bn)) / g_stage_bytes(bn, pair) > 8
-             ? 8
-             : (kGSmemLimit - g_fixed(bn)) / g_stage_bytes(bn, pair);
+  return (kGSmemLimit - kGFixed) / g_stage_bytes(bn, pair);
 }
 __host__ __device__ constexpr size_t g_smem(int bn, bool pair) {
-  return static_cast<size_t>(g_fixed(bn)) + g_stages(bn, pair) * g_stage_bytes(bn, pair);
+  return static_cast<size_t>(kGFixed) + g_stages(bn, pair) * g_stage_bytes(bn, pair);
 }
 
 }  // namespace
@@ -73,9 +73,9 @@ __global__ void __launch_bounds__(kGThreads, 1)
   constexpr uint32_t kTxScales = (PAIR ? 2 : 1) * kSBytes;
   constexpr int NACC = 2 * BN + 32 <= 512 ? 2 : 1;  // accumulators that fit beside the scales
   constexpr uint32_t kScaleCol = NACC * BN;         // two sets of 4 (A) + 8 (B) columns
-  constexpr int kCols = BN / 2;                     // columns of one epilogue warp
+  constexpr int kCols = BN / 4;                     // columns of one epilogue warp
   static_assert(STAGES >= 3, "pipeline depth");
-  static_assert(OUT != kOutQ8 || kCols == kQBlock, "one block per epilogue thread");
+  static_assert(kCols == 32 || kCols == 64, "epilogue columns");
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -83,7 +83,10 @@ __global__ void __launch_bounds__(kGThreads, 1)
   uint8_t* sA = smem;
   uint8_t* sB = sA + STAGES * kGABytes;
   uint8_t* sBox = sB + STAGES * kBBytes;
-  uint8_t* sS = sBox + kGEpiWarps * kGBoxes * kGBoxBytes;
+  uint8_t* sBias = sBox + kGEpiWarps * kGBoxBytes;      // [warp][64] bf16
+  volatile uint64_t* sMax =                              // [2][warp][32] (turn, magnitude)
+      reinterpret_cast<volatile uint64_t*>(sBias + kGEpiWarps * 128);
+  uint8_t* sS = sBox + kGEpiBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(sS + STAGES * kSBytes);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
@@ -113,14 +116,14 @@ __global__ void __launch_bounds__(kGThreads, 1)
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 8 && lane == 0) {
+  if (warp == kGProducer && lane == 0) {
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
     tma_prefetch_desc(&tmSA);
     tma_prefetch_desc(&tmSB);
     if (!p.direct) tma_prefetch_desc(&tmOut);
   }
-  if (warp == 9) {
+  if (warp == kGIssuer) {
     if constexpr (PAIR) {
       tmem_alloc_pair(tmem_slot, 512);
       tmem_relinquish_pair();
@@ -128,6 +131,10 @@ __global__ void __launch_bounds__(kGThreads, 1)
       tmem_alloc(tmem_slot, 512);
       tmem_relinquish();
     }
+  }
+  if (OUT == kOutQ8 && warp < kGEpiWarps) {
+    sMax[warp * 32 + lane] = 0;
+    sMax[(kGEpiWarps + warp) * 32 + lane] = 0;
   }
   pdl_trigger();
   pdl_wait();
@@ -141,7 +148,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   const WaitCtl wc{abort_flag, p.err, p.timeout_ns};
 
-  if (warp == 8) {
+  if (warp == kGProducer) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       int stage = 0;
@@ -201,7 +208,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == kGIssuer) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0 && leader) {
       int stage = 0;
@@ -272,17 +279,25 @@ __global__ void __launch_bounds__(kGThreads, 1)
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, grp = warp >> 2;
-    uint8_t* box = sBox + warp * kGBoxes * kGBoxBytes;
+    uint8_t* box = sBox + warp * kGBoxBytes;
+    const uint32_t box_u32 = smem_u32(box), bias_u32 = smem_u32(sBias + warp * 128);
     constexpr int ES = OUT == kOutQ8 ? 1 : OUT == kOutBf16 ? 2 : 4;  // bytes of an output element
-    constexpr int BC = 64 / ES;                                      // columns of a box
+    constexpr int BC = 64 / ES < kCols ? 64 / ES : kCols;            // columns of a box
     constexpr int NB = kCols / BC;                                   // boxes of a tile
     int acc = 0;
     uint32_t acc_phase = 0;
-    int slot = 0;
+    uint32_t turn = 0;  // 8-bit output: tiles whose maxima this warp has exchanged
     for (int tile = unit0; tile < p.num_tiles; tile += units) {
       const int m_blk = tile / p.n_blocks, n_blk = tile % p.n_blocks;
       const int row0 = m_blk * kTileM + static_cast<int>(rank) * kGM + q * 32;
       const int col0 = n_blk * BN + grp * kCols;
+      if (p.bias != nullptr && 2 * lane < kCols) {  // this warp's biases, while the tile runs
+        const int c = col0 + 2 * lane;
+        uint32_t b = 0;
+        if (c + 1 < p.N) b = __ldg(reinterpret_cast<const uint32_t*>(p.bias + c));
+        else if (c < p.N) b = __ldg(reinterpret_cast<const uint16_t*>(p.bias + c));
+        reinterpret_cast<uint32_t*>(sBias + warp * 128)[lane] = b;
+      }
       int ok = 1;
       if (lane == 0) ok = wait_bounded(&tfull[acc], acc_phase, wc) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -307,32 +322,25 @@ __global__ void __launch_bounds__(kGThreads, 1)
       }
       if (++acc == NACC) { acc = 0; acc_phase ^= 1u; }
       const int row = row0 + lane;
-      const bool live = row0 < p.M && col0 < p.N;  // the warp holds part of the output
-      if (!live) continue;
+      // does the warp (for 8-bit blocks, any warp of its block of 128) hold part of the output?
+      if (row0 >= p.M || (OUT == kOutQ8 ? col0 & ~(kQBlock - 1) : col0) >= p.N) continue;
 
-      // bias and activation, 32 columns at a time
 #pragma unroll
       for (int i = 0; i < kCols / 32; ++i) {
-        const int c = col0 + 32 * i;
         if (p.bias != nullptr) {
-          if (c + 32 <= p.N) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              const uint4 b4 = __ldg(reinterpret_cast<const uint4*>(p.bias + c) + v);
-              const uint32_t bw[4] = {b4.x, b4.y, b4.z, b4.w};
+          for (int v = 0; v < 4; ++v) {
+            const uint4 b4 = lds128(bias_u32 + i * 64 + v * 16);
+            const uint32_t bw[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float& a = reinterpret_cast<float&>(r[i][8 * v + 2 * e]);
-                float& b = reinterpret_cast<float&>(r[i][8 * v + 2 * e + 1]);
-                a += bf16lo(bw[e]);
-                b += bf16hi(bw[e]);
-              }
+            for (int e = 0; e < 4; ++e) {
+              uint32_t& lo = r[i][8 * v + 2 * e];
+              uint32_t& hi = r[i][8 * v + 2 * e + 1];
+              const float2 z = f2unpack(
+                  fadd2((static_cast<uint64_t>(hi) << 32) | lo, bf16x2_to_f2(bw[e])));
+              lo = __float_as_uint(z.x);
+              hi = __float_as_uint(z.y);
             }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c + e < p.N)
-                r[i][e] = __float_as_uint(__uint_as_float(r[i][e]) + __bfloat162float(p.bias[c + e]));
           }
         }
         if (p.gelu) {
@@ -354,23 +362,25 @@ __global__ void __launch_bounds__(kGThreads, 1)
 
       float inv = 0.f;
       if constexpr (OUT == kOutQ8) {
-        // this thread's 128 columns of the row are one block; columns past N hold no value
+        // A block of a row is shared by the same lane of 128 / kCols warps, which exchange its
+        // largest magnitude; columns past N hold no value.
+        constexpr int S = kQBlock / kCols;
         if (col0 + kCols > p.N) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < kCols / 32; ++i)
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (col0 + 32 * i + e >= p.N) r[i][e] = 0;
         }
         uint32_t a = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < kCols / 32; ++i)
 #pragma unroll
           for (int e = 0; e < 32; ++e) a = max(a, r[i][e] & 0x7FFFFFFFu);
         if (a >= kInfBits) {
           a = 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < kCols / 32; ++i)
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const float f = __uint_as_float(r[i][e]);
@@ -378,22 +388,47 @@ __global__ void __launch_bounds__(kGThreads, 1)
               r[i][e] = __float_as_uint(inf_to_nan(f));
             }
         }
+        // Each lane publishes its magnitude with the tile's turn and polls its partners' (as
+        // bounded as every wait here, which a named barrier is not). Two slots by turns: a
+        // warp writes one again only after its partners have read it, since it needs their
+        // magnitudes of the turn between.
+        ++turn;
+        volatile uint64_t* mx = sMax + (turn & 1u) * kGEpiWarps * 32;
+        mx[warp * 32 + lane] = (static_cast<uint64_t>(turn) << 32) | a;
+#pragma unroll
+        for (int k = 1; k < S; ++k) {
+          const int other = q + 4 * (grp / S * S + (grp + k) % S);
+          uint64_t v = mx[other * 32 + lane], t0 = 0;
+          for (uint32_t i = 1; static_cast<uint32_t>(v >> 32) != turn; ++i) {
+            if ((i & 255u) == 0) {
+              if (t0 == 0) t0 = global_timer_ns();
+              if (*abort_flag) break;
+              if (global_timer_ns() - t0 > p.timeout_ns) {
+                *abort_flag = 1;
+                atomicCAS(p.err, 0, static_cast<int>(RS_ERR_DEVICE_TIMEOUT));
+                break;
+              }
+            }
+            v = mx[other * 32 + lane];
+          }
+          a = max(a, static_cast<uint32_t>(v));
+        }
+        __syncwarp();
         const uint32_t byte = e8m0_byte(a);
         inv = e8m0_inverse(byte);
-        if (row < p.M) p.out_scales[scale_offset(row, col0 >> 7, p.kqo)] = static_cast<uint8_t>(byte);
+        if (row < p.M && grp % S == 0)
+          p.out_scales[scale_offset(row, col0 >> 7, p.kqo)] = static_cast<uint8_t>(byte);
       }
 
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const int c = col0 + b * BC;
         if (c >= p.N) break;
-        uint8_t* bx = box + slot * kGBoxBytes;
-        const uint32_t bx_u32 = smem_u32(bx);
-        uint32_t w[16];  // the row's 64 bytes
+        uint32_t w[BC * ES / 4];  // this row of the box
         if constexpr (OUT == kOutQ8) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int k = b * 64 + 4 * e;
+          for (int e = 0; e < BC / 4; ++e) {
+            const int k = b * BC + 4 * e;
             w[e] = e4m3x4(__uint_as_float(r[k / 32][k % 32]) * inv,
                           __uint_as_float(r[k / 32][k % 32 + 1]) * inv,
                           __uint_as_float(r[k / 32][k % 32 + 2]) * inv,
@@ -436,7 +471,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
             }
           }
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
+          for (int e = 0; e < BC * ES / 4; ++e) {
             if constexpr (OUT == kOutBf16)
               w[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
             else
@@ -444,11 +479,15 @@ __global__ void __launch_bounds__(kGThreads, 1)
           }
         }
         // the store that last used this box has read it
-        if (lane == 0) bulk_wait_group_read<kGBoxes - 1>();
+        if (lane == 0) bulk_wait_group_read0();
         __syncwarp();
+        // 64-byte rows in the 64-byte swizzle (32-byte rows, 8-bit blocks of narrow tiles, in
+        // the 32-byte one)
+        constexpr int U = BC * ES / 16;  // 16-byte units of a row
+        const uint32_t sw = U == 4 ? (lane >> 1) & 3 : (lane >> 2) & 1;
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          sts128(bx_u32 + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4),
+        for (int u = 0; u < U; ++u)
+          sts128(box_u32 + lane * (16 * U) + ((u ^ sw) << 4),
                  make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]));
         // TMA stores whole 16-byte units: where the last columns end inside one, they and rows
         // that TMA cannot address (a pitch or base off 16 bytes) go by plain stores,
@@ -457,28 +496,26 @@ __global__ void __launch_bounds__(kGThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_2d(&tmOut, bx, c, row0);
+            tma_store_2d(&tmOut, box, c, row0);
             bulk_commit_group();
           }
-        } else {
+        } else if constexpr (OUT != kOutQ8) {
           __syncwarp();
 #pragma unroll 4
           for (int it = 0; it < BC; ++it) {
             const int idx = it * 32 + lane, rr = idx / BC, cc = idx % BC;
-            const uint8_t* src = bx + rr * 64 + ((((cc * ES) >> 4) ^ ((rr >> 1) & 3)) << 4) + ((cc * ES) & 15);
+            const uint8_t* src = box + rr * 64 + ((((cc * ES) >> 4) ^ ((rr >> 1) & 3)) << 4) + ((cc * ES) & 15);
             if (row0 + rr < p.M && c + cc < p.N) {
               uint8_t* dst = static_cast<uint8_t*>(p.out) +
                              (static_cast<int64_t>(row0 + rr) * p.ldo + c + cc) * ES;
               if constexpr (ES == 2)
                 *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(src);
-              else if constexpr (ES == 4)
+              else
                 *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(src);
             }
           }
           __syncwarp();
-          if (lane == 0) bulk_commit_group();  // an empty group keeps the boxes' turns
         }
-        slot ^= 1;
       }
     }
     if (lane == 0) bulk_wait_group0();
@@ -493,7 +530,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
       spin_ns(1000000);
     cluster_sync();
   }
-  if (warp == 9) {
+  if (warp == kGIssuer) {
     tc_fence_after_sync();
     if constexpr (PAIR)
       tmem_dealloc_pair(tmem_base, 512);
@@ -551,11 +588,13 @@ int go(Fp8Gemm p, int num_sms, cudaStream_t s, bool pdl) {
   if (st == RS_OK) st = tmap_scales(&tSA, p.sa, p.M, p.K, 1);
   if (st == RS_OK) st = tmap_scales(&tSB, p.sb, p.N, p.K, g_scale_tiles_b(BN));
   constexpr int es = OUT == kOutQ8 ? 1 : OUT == kOutBf16 ? 2 : 4;
+  constexpr int box = 64 / es < BN / 4 ? 64 / es : BN / 4;  // the epilogue's boxes
   if (st == RS_OK && !p.direct)
     st = tmap_2d(&tO, OUT == kOutQ8     ? u8
                       : OUT == kOutBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                 es, p.out, p.N, p.M, p.ldo, 64 / es, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+                 es, p.out, p.N, p.M, p.ldo, box, 32,
+                 box * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
   if (st != RS_OK) return st;
   auto kern = fp8_gemm_kernel<BN, PAIR, OUT>;
   constexpr size_t smem = g_smem(BN, PAIR);
@@ -599,14 +638,14 @@ int go(Fp8Gemm p, int num_sms, cudaStream_t s, bool pdl) {
   return RS_OK;
 }
 
+// Tiles of 128 x 128 while one wave of them covers the output: more SMs share a small product
+// and each epilogue is short. Else CTA pairs on 256 x 256 (256 x 128 for narrow outputs).
 template <int OUT>
 int pick(const Fp8Gemm& p, int num_sms, cudaStream_t s, bool pdl) {
-  const bool pair = p.M > 128;
-  if constexpr (OUT != kOutQ8) {
-    if (p.N <= 128)
-      return pair ? go<128, true, OUT>(p, num_sms, s, pdl) : go<128, false, OUT>(p, num_sms, s, pdl);
-  }
-  return pair ? go<256, true, OUT>(p, num_sms, s, pdl) : go<256, false, OUT>(p, num_sms, s, pdl);
+  const int64_t small = (static_cast<int64_t>(p.M) + 127) / 128 * ((static_cast<int64_t>(p.N) + 127) / 128);
+  if (small <= num_sms || p.M <= 128) return go<128, false, OUT>(p, num_sms, s, pdl);
+  if (p.N <= 128) return go<128, true, OUT>(p, num_sms, s, pdl);
+  return go<256, true, OUT>(p, num_sms, s, pdl);
 }
 
 }  // namespace
