@@ -150,19 +150,19 @@ __global__ void __launch_bounds__(kGThreads, 1)
 
   if (warp == kGProducer) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      uint32_t pend_mask = 0, pend_phase = 0;
-      const uint32_t full_leader = PAIR ? mapa_shared(smem_u32(&full[0]), 0u) : 0u;
-      for (int tile = unit0; tile < p.num_tiles; tile += units) {
-        const int m_blk = tile / p.n_blocks, n_blk = tile % p.n_blocks;
-        const int a_row = m_blk * kTileM + static_cast<int>(rank) * kGM;
-        const int n0 = n_blk * BN;
-        const int b_row = n0 + static_cast<int>(rank) * kBRows;
-        bool ok = true;
-        for (int kb = 0; kb < KB; ++kb) {
-          if (!wait_bounded(&empty[stage], phase ^ 1u, wc)) { ok = false; break; }
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t pend_mask = 0, pend_phase = 0;
+    const uint32_t full_leader = PAIR ? mapa_shared(smem_u32(&full[0]), 0u) : 0u;
+    for (int tile = unit0; tile < p.num_tiles; tile += units) {
+      const int m_blk = tile / p.n_blocks, n_blk = tile % p.n_blocks;
+      const int a_row = m_blk * kTileM + static_cast<int>(rank) * kGM;
+      const int n0 = n_blk * BN;
+      const int b_row = n0 + static_cast<int>(rank) * kBRows;
+      bool ok = true;
+      for (int kb = 0; kb < KB; ++kb) {
+        if (!warp_wait(&empty[stage], phase ^ 1u, wc)) { ok = false; break; }
+        if (elect_one()) {
           const bool scales = (kb & 3) == 0;
           if (leader) mbar_arrive_expect_tx(&full[stage], scales ? kTx + kTxScales : kTx);
           uint8_t* dA = sA + stage * kGABytes;
@@ -186,93 +186,108 @@ __global__ void __launch_bounds__(kGThreads, 1)
               tma_load_3d(dS + kScaleTile, &tmSB, &full[stage], 0, kb >> 2, n0 >> 7);
             }
           }
-          const uint32_t bit = 1u << stage;
-          pend_mask |= bit;
-          pend_phase = (pend_phase & ~bit) | (phase << stage);
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
-        if (!ok) break;
+        __syncwarp();
+        const uint32_t bit = 1u << stage;
+        pend_mask |= bit;
+        pend_phase = (pend_phase & ~bit) | (phase << stage);
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
-      // every copy must land before the CTA may exit (a pair's land on the leader's barriers)
-      if (leader) {
+      if (!ok) break;
+    }
+    // every copy must land before the CTA may exit (a pair's land on the leader's barriers)
+    if (leader) {
 #pragma unroll
-        for (int s = 0; s < STAGES; ++s)
-          if (pend_mask & (1u << s)) wait_bounded(&full[s], (pend_phase >> s) & 1u, wc, false);
-      }
-      if constexpr (PAIR) {
-        // and the leader's releases of every stage must have arrived here
-        for (int i = 0; i < STAGES; ++i) {
-          if (!wait_bounded(&empty[stage], phase ^ 1u, wc)) break;
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-        }
+      for (int s = 0; s < STAGES; ++s)
+        if (pend_mask & (1u << s)) warp_wait(&full[s], (pend_phase >> s) & 1u, wc, false);
+    }
+    if constexpr (PAIR) {
+      // and the leader's releases of every stage must have arrived here
+      for (int i = 0; i < STAGES; ++i) {
+        if (!warp_wait(&empty[stage], phase ^ 1u, wc)) break;
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
     }
-    __syncwarp();
   } else if (warp == kGIssuer) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && leader) {
+    if (leader) {
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
       uint32_t set = 0;  // scale columns in use
+      uint32_t ts = 0;
       bool issued = false;
+      const uint64_t ad0 = sw128_kmajor_desc(smem_u32(sA));
+      const uint64_t bd0 = sw128_kmajor_desc(smem_u32(sB));
+      const uint64_t sd0 = scale_tile_desc(smem_u32(sS));
       for (int tile = unit0; tile < p.num_tiles; tile += units) {
         const int n0 = (tile % p.n_blocks) * BN;
-        if (!wait_bounded(&tempty[acc], acc_phase ^ 1u, wc, true, PAIR)) break;
+        if (!warp_wait(&tempty[acc], acc_phase ^ 1u, wc, true, PAIR)) break;
         tc_fence_after_sync();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
-        uint32_t ts = 0;
+        // B's columns start inside a scale tile when BN is no multiple of 128: 32 rows a column
+        const uint32_t bcol = 4u + static_cast<uint32_t>((n0 & 127) >> 5);
         bool ok = true;
         for (int kb = 0; kb < KB; ++kb) {
-          if (!wait_bounded(&full[stage], phase, wc)) { ok = false; break; }
+          if (!warp_wait(&full[stage], phase, wc)) { ok = false; break; }
           tc_fence_after_sync();
           if ((kb & 3) == 0) {
             ts = tmem_base + kScaleCol + set * 16u;
             set ^= 1u;
-            const uint64_t sd = scale_tile_desc(smem_u32(sS + stage * kSBytes));
-#pragma unroll
-            for (int i = 0; i < 1 + kSTiles; ++i) {
-              if constexpr (PAIR)
-                tmem_cp_scales_pair(ts + 4u * i, sd + static_cast<uint64_t>(i * (kScaleTile >> 4)));
-              else
-                tmem_cp_scales(ts + 4u * i, sd + static_cast<uint64_t>(i * (kScaleTile >> 4)));
-            }
           }
-          // B's columns start inside a scale tile when BN is no multiple of 128: 32 rows a column
-          const uint32_t tsb = ts + 4u + static_cast<uint32_t>((n0 & 127) >> 5);
           const uint32_t id = idesc_mx_byte(kIdesc, static_cast<uint32_t>(kb & 3));
-          const uint64_t ad = sw128_kmajor_desc(smem_u32(sA + stage * kGABytes));
-          const uint64_t bd = sw128_kmajor_desc(smem_u32(sB + stage * kBBytes));
+          const uint64_t ad = ad0 + static_cast<uint64_t>(stage * (kGABytes >> 4));
+          const uint64_t bd = bd0 + static_cast<uint64_t>(stage * (kBBytes >> 4));
+          const int steps = (p.K - kb * kGK + 31) / 32;  // whole 32-wide steps past K hold zeros
+          if (elect_one()) {
+            if ((kb & 3) == 0) {
+              const uint64_t sd = sd0 + static_cast<uint64_t>(stage * (kSBytes >> 4));
 #pragma unroll
-          for (int k = 0; k < kGK / 32; ++k) {
-            // whole 32-wide steps past K hold zeros: left out
-            if (k > 0 && kb * kGK + k * 32 >= p.K) break;
+              for (int i = 0; i < 1 + kSTiles; ++i) {
+                if constexpr (PAIR)
+                  tmem_cp_scales_pair(ts + 4u * i, sd + static_cast<uint64_t>(i * (kScaleTile >> 4)));
+                else
+                  tmem_cp_scales(ts + 4u * i, sd + static_cast<uint64_t>(i * (kScaleTile >> 4)));
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < kGK / 32; ++k) {
+              if (k == 0 || k < steps) {
+                if constexpr (PAIR)
+                  umma_mx_pair(d_tmem, ad + 2u * k, bd + 2u * k, id, ts, ts + bcol, (kb | k) != 0 ? 1u : 0u);
+                else
+                  umma_mx(d_tmem, ad + 2u * k, bd + 2u * k, id, ts, ts + bcol, (kb | k) != 0 ? 1u : 0u);
+              }
+            }
             if constexpr (PAIR)
-              umma_mx_pair(d_tmem, ad + 2u * k, bd + 2u * k, id, ts, tsb, (kb | k) != 0 ? 1u : 0u);
+              umma_commit_pair_mc(&empty[stage], 0x3);
             else
-              umma_mx(d_tmem, ad + 2u * k, bd + 2u * k, id, ts, tsb, (kb | k) != 0 ? 1u : 0u);
+              umma_commit(&empty[stage]);
           }
+          __syncwarp();
           issued = true;
-          if constexpr (PAIR)
-            umma_commit_pair_mc(&empty[stage], 0x3);
-          else
-            umma_commit(&empty[stage]);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
-        if constexpr (PAIR)
-          umma_commit_pair_mc(&tfull[acc], 0x3);
-        else
-          umma_commit(&tfull[acc]);
+        if (elect_one()) {
+          if constexpr (PAIR)
+            umma_commit_pair_mc(&tfull[acc], 0x3);
+          else
+            umma_commit(&tfull[acc]);
+        }
+        __syncwarp();
         if (++acc == NACC) { acc = 0; acc_phase ^= 1u; }
       }
-      if (*abort_flag && issued) {
-        if constexpr (PAIR)
-          umma_commit_pair(drain);
-        else
-          umma_commit(drain);
-        wait_bounded(drain, 0u, wc, false);
+      if (__any_sync(0xffffffffu, *abort_flag != 0) && issued) {
+        if (elect_one()) {
+          if constexpr (PAIR)
+            umma_commit_pair(drain);
+          else
+            umma_commit(drain);
+        }
+        __syncwarp();
+        warp_wait(drain, 0u, wc, false);
       }
     }
     __syncwarp();

@@ -102,6 +102,24 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, con
   }
 }
 
+// True in one lane of a converged warp, the same one every time. Code that the whole warp runs,
+// with only the tcgen05 and TMA instructions under this predicate, keeps their operands in
+// uniform registers; under `lane == 0` each of them is assembled lane by lane.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+// wait_bounded by every lane of a converged warp, with one answer for all of them.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& w,
+                                          bool honor_abort = true, bool cluster = false) {
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, w, honor_abort, cluster)) != 0;
+}
+
 // Busy-waits about `ns` nanoseconds.
 __device__ __forceinline__ void spin_ns(uint64_t ns) {
   const uint64_t t0 = global_timer_ns();
