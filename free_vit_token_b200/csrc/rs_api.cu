@@ -12,7 +12,7 @@
 #include <cuda_runtime.h>
 
 #include "rs.h"
-#include "rs_internal.h"
+#include "rs_ops.h"
 
 namespace rs {
 

@@ -21,6 +21,13 @@
 
 namespace rs {
 
+// Products of two fp32 pairs (the sums are in rs_ptx.cuh).
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 constexpr int kQBlock = 128;      // values per scale
 constexpr int kScaleTile = 512;   // bytes of scales for 128 rows x 4 blocks
 

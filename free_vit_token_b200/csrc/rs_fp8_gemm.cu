@@ -24,12 +24,31 @@
 
 #include "rs_fp8.cuh"
 #include "rs_gelu.cuh"
-#include "rs_internal.h"
-#include "rs_ptx.cuh"
+#include "rs_gelu_logit.h"
+#include "rs_ops.h"
+#include "rs_ptx_mx.cuh"
 
 namespace rs {
 
 namespace {
+
+// GELU of two fp32 lanes through a logistic form of the normal CDF (rs_gelu_logit.h, max
+// |error| 1.4e-5): half the FMAs of the polynomials of rs_gelu.cuh, and two instructions of the
+// exponential unit per value.
+__device__ __forceinline__ uint64_t gelu2_logit(uint64_t z2) {
+  const float2 s = f2unpack(mul2(z2, z2));
+  const uint64_t t = f2pack(fminf(s.x, RS_GELU_LOGIT_T), fminf(s.y, RS_GELU_LOGIT_T));
+  uint64_t q = kpair(-RS_GELU_LOGIT_Q3);
+  q = ffma2(q, t, kpair(-RS_GELU_LOGIT_Q2));
+  q = ffma2(q, t, kpair(-RS_GELU_LOGIT_Q1));
+  q = ffma2(q, t, kpair(-RS_GELU_LOGIT_Q0));
+  const float2 x = f2unpack(mul2(q, z2));
+  const float2 d = f2unpack(fadd2(f2pack(ex2_approx(x.x), ex2_approx(x.y)), kpair(1.f)));
+  float rx, ry;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rx) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ry) : "f"(d.y));
+  return mul2(z2, f2pack(rx, ry));
+}
 
 constexpr int kGM = 128;                       // rows of A per CTA and tile
 constexpr int kGK = 128;                       // K elements (bytes) per stage
@@ -365,7 +384,16 @@ __global__ void __launch_bounds__(kGThreads, 1)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               z2[e] = (static_cast<uint64_t>(r[i][16 * h + 2 * e + 1]) << 32) | r[i][16 * h + 2 * e];
-            gelu2_block<8>(z2, g2);
+            // half of the columns by either form: the FMA and the exponential unit share the work
+            uint64_t zp[4], gp[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              zp[e] = z2[e];
+              g2[4 + e] = gelu2_logit(z2[4 + e]);
+            }
+            gelu2_block<4>(zp, gp);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) g2[e] = gp[e];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               r[i][16 * h + 2 * e] = static_cast<uint32_t>(g2[e]);
@@ -654,13 +682,17 @@ int go(Fp8Gemm p, int num_sms, cudaStream_t s, bool pdl) {
 }
 
 // Tiles of 128 x 128 while one wave of them covers the output: more SMs share a small product
-// and each epilogue is short. Else CTA pairs on 256 x 256 (256 x 128 for narrow outputs).
+// and each epilogue is short. Else 256 columns, by single CTAs while the reduction is short (a
+// pair's accumulator goes back and forth between two SMs once a tile) and by CTA pairs on 256
+// rows past that (a third less operand traffic). Measured 16384 x 4096, single / pair, us: plain
+// K = 512 42 / 49, K = 768 61 / 55; GELU K = 768 64 / 67, K = 1536 104 / 98.
 template <int OUT>
 int pick(const Fp8Gemm& p, int num_sms, cudaStream_t s, bool pdl) {
   const int64_t small = (static_cast<int64_t>(p.M) + 127) / 128 * ((static_cast<int64_t>(p.N) + 127) / 128);
   if (small <= num_sms || p.M <= 128) return go<128, false, OUT>(p, num_sms, s, pdl);
-  if (p.N <= 128) return go<128, true, OUT>(p, num_sms, s, pdl);
-  return go<256, true, OUT>(p, num_sms, s, pdl);
+  const bool pair = p.K > (p.gelu ? 1024 : 512);
+  if (p.N <= 128) return pair ? go<128, true, OUT>(p, num_sms, s, pdl) : go<128, false, OUT>(p, num_sms, s, pdl);
+  return pair ? go<256, true, OUT>(p, num_sms, s, pdl) : go<256, false, OUT>(p, num_sms, s, pdl);
 }
 
 }  // namespace

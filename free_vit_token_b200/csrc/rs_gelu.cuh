@@ -12,6 +12,11 @@
 
 namespace rs {
 
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ uint64_t kpair(float c) { return f2pack(c, c); }
 
 // Exact (erf) GELU of two fp32 lanes, GELU(z) = z * Phi(z), evaluated with the

@@ -221,106 +221,4 @@ int attn_kv_box_rows();
 cudaError_t launch_attn(const CUtensorMap& tmQ, const CUtensorMap& tmKV, const AttnParams& p,
                         cudaStream_t stream, bool pdl = false);
 
-// ---------------------------------------------------------------- layer norm, 8-bit blocks
-// The current device's SM count (cached; allocates nothing) and status flag (allocated on a
-// device's first use): RS_OK or an error. Defined beside the library's device state.
-int device_sms(int* num_sms);
-int device_flag(int* num_sms, int** err);
-
-// Layer norm forward (rs_norm.cu): y (or q and scales, by launcher) and optional row stats.
-struct LnForward {
-  const void* x;
-  int64_t ldx;         // elements between rows
-  int M, C;
-  const void* gamma;   // [C] or null (ones)
-  const void* beta;    // [C] or null (zeros)
-  bool p32;            // gamma and beta are fp32 (else x's type)
-  float eps;
-  void* y;
-  int64_t ldy;
-  float2* stats;       // [M] (mean, rstd) or null
-  uint8_t* q;          // quantised output: e4m3 rows, ldq bytes apart
-  int64_t ldq;
-  uint8_t* scales;     // scale tiles (rs_fp8.cuh)
-  int kq;              // scale tiles along C
-};
-struct LnBackward {
-  const void* dy;
-  int64_t lddy;
-  const void* x;
-  int64_t ldx;
-  const void* dres;    // added to dx, or null
-  int64_t lddres;
-  const float2* stats;
-  const void* gamma;
-  bool p32;
-  int M, C;
-  void* dx;            // or null
-  int64_t lddx;
-  float* partials;     // [blocks][2][C], or null: no dgamma, dbeta
-};
-// `vec`: every row of every tensor starts on 16 bytes and is a whole number of 16-byte vectors.
-cudaError_t launch_ln_forward(const LnForward& p, int dtype, bool vec, int num_sms,
-                              cudaStream_t s);
-cudaError_t launch_ln_quantize(const LnForward& p, int dtype, int num_sms, cudaStream_t s);
-// Backward, then the sum of the blocks' partials (at most num_sms) into dgamma, dbeta.
-cudaError_t launch_ln_backward(const LnBackward& p, int dtype, bool vec, int num_sms, float* dgamma,
-                               float* dbeta, cudaStream_t s);
-// out[c] = sum_p partials[p][c], p ascending by eights, for n columns: the first `split` of
-// them to out0, the others to out1 (either may be null).
-cudaError_t launch_col_reduce(const float* partials, int P, int n, int split, float* out0,
-                              float* out1, cudaStream_t stream, bool pdl);
-
-// Quantisation (rs_quant.cu): rows in blocks along K, and/or the transposed tensor in blocks
-// along the rows, and/or the column sums' partials.
-struct Quant {
-  const void* x;
-  int64_t ldx;
-  int rows, K;
-  uint8_t* q;          // [rows][ldq] or null
-  int64_t ldq;
-  uint8_t* scales;
-  uint8_t* qt;         // [K][ldqt] or null
-  int64_t ldqt;
-  uint8_t* scales_t;
-  float* partials;     // [quant_chunks(rows, K)][K] column sums, or null
-};
-// Blocks that share out the row tiles of 128 of one column tile: about four per SM in all (two
-// are resident, and a block loads its next tile while it works on one).
-inline int quant_chunks(int rows, int K) {
-  const int tiles = (rows + 127) / 128, cols = (K + 127) / 128;
-  const int most = cols < 592 ? (592 + cols - 1) / cols : 1;
-  return tiles < most ? tiles : most;
-}
-cudaError_t launch_quantize(const Quant& p, int dtype, bool vec, cudaStream_t s, bool pdl = false);
-
-// The product of two quantised operands (rs_fp8_gemm.cu): out = act(A B^T + bias) + resid.
-constexpr int kOutBf16 = 0;
-constexpr int kOutFp32 = 1;
-constexpr int kOutQ8 = 2;
-struct Fp8Gemm {
-  const void* a;         // [M][lda] e4m3
-  int64_t lda;
-  const void* sa;        // scale tiles of a
-  const void* b;         // [N][ldb] e4m3
-  int64_t ldb;
-  const void* sb;
-  int M, N, K;
-  const __nv_bfloat16* bias;  // [N] or null
-  int gelu;              // 1: exact GELU after the bias
-  const void* resid;     // [M][ldr] of the output's type, or null (not with kOutQ8)
-  int64_t ldr;
-  int rvec;              // resid's rows start on 16 bytes
-  void* out;             // [M][ldo] bf16, fp32 or e4m3
-  int64_t ldo;
-  int direct;            // out's rows do not start on 16 bytes: plain stores, not TMA
-  uint8_t* out_scales;   // kOutQ8: scale tiles of out
-  int kqo;               // kOutQ8: scale tiles along N
-  int* err;
-  unsigned long long timeout_ns;
-  int n_blocks, num_tiles;  // set by the launcher
-};
-// RS_OK or an error status.
-int launch_fp8_gemm(const Fp8Gemm& p, int out, int num_sms, cudaStream_t s, bool pdl = false);
-
 }  // namespace rs

@@ -26,7 +26,7 @@
 #include <cuda_runtime.h>
 
 #include "rs_fp8.cuh"
-#include "rs_internal.h"
+#include "rs_ops.h"
 #include "rs_ptx.cuh"
 
 namespace rs {
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(fwd_threads(TPR), TPR <= 256 ? 2 : 1)
       beta.get(i, b);
 #pragma unroll
       for (int e = 0; e < E / 2; ++e) {
-        const float2 v = f2unpack(ffma2(fmul2(fadd2(f2[e], nmean), rstd2), g[e], b[e]));
+        const float2 v = f2unpack(ffma2(mul2(fadd2(f2[e], nmean), rstd2), g[e], b[e]));
         f[2 * e] = v.x;
         f[2 * e + 1] = v.y;
       }
@@ -539,8 +539,8 @@ __global__ void __launch_bounds__(bwd_threads(TPR, VPL * Elem<T>::E), 1)
       gamma.get(i, g);
 #pragma unroll
       for (int e = 0; e < E / 2; ++e) {
-        const uint64_t xh = fmul2(fadd2(fx[e], nmean), rstd);
-        const uint64_t w = fmul2(fy[e], g[e]);
+        const uint64_t xh = mul2(fadd2(fx[e], nmean), rstd);
+        const uint64_t w = mul2(fy[e], g[e]);
         w2 = fadd2(w2, w);
         wx2 = ffma2(w, xh, wx2);
         dg2[i * E / 2 + e] = ffma2(fy[e], xh, dg2[i * E / 2 + e]);
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(bwd_threads(TPR, VPL * Elem<T>::E), 1)
       gamma.get(i, g);
 #pragma unroll
       for (int e = 0; e < E / 2; ++e) {
-        const uint64_t xh = fmul2(fadd2(fx[e], nmean), rstd);
+        const uint64_t xh = mul2(fadd2(fx[e], nmean), rstd);
         const float2 v = f2unpack(ffma2(rstd, ffma2(xh, nm2, ffma2(fy[e], g[e], nm1)), fr[e]));
         o[2 * e] = v.x;
         o[2 * e + 1] = v.y;

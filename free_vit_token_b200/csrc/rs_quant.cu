@@ -14,7 +14,7 @@
 #include <cuda_runtime.h>
 
 #include "rs_fp8.cuh"
-#include "rs_internal.h"
+#include "rs_ops.h"
 #include "rs_ptx.cuh"
 
 namespace rs {
