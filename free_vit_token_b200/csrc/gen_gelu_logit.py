@@ -6,9 +6,8 @@ z^2; it is fitted here to logit(Phi(z)) / (z ln 2) by Lawson's iteratively rewei
 squares on Chebyshev nodes in t, weighted by the error it causes in GELU (z^2 Phi (1 - Phi)).
 Past sqrt(T) Q keeps its last value, where 1 - Phi < 3e-7.
 
-It costs half the FMAs of the polynomial form of rs_gelu_poly.h and two exponential-unit
-instructions per value instead, so that an epilogue that takes each form for half of its
-columns keeps both units busy.
+It costs half the FMAs of the polynomial form of rs_gelu_poly.h and three exponential-unit
+instructions per two values instead, and needs no choice by range.
 
 Run: python gen_gelu_logit.py > rs_gelu_logit.h
 """
