@@ -398,11 +398,8 @@ __global__ void __launch_bounds__(fwd_threads(TPR), TPR <= 256 ? 2 : 1)
     if (live && l == 0 && p.stats != nullptr) p.stats[row] = make_float2(mean, rstd);
     T* y = static_cast<T*>(p.y) + static_cast<int64_t>(row) * p.ldy;
     const int yof = VEC ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(y) & 15);
-    if constexpr (!VEC && !QUANT) group_barrier<TPR>(group);  // the slot is read: y takes its place
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
+    auto affine = [&](int i, float (&f)[E]) {
       uint64_t f2[E / 2], g[E / 2], b[E / 2];
-      float f[E];
       Elem<T>::pairs(cur[i], f2);
       gamma.get(i, g);
       beta.get(i, b);
@@ -412,36 +409,56 @@ __global__ void __launch_bounds__(fwd_threads(TPR), TPR <= 256 ? 2 : 1)
         f[2 * e] = v.x;
         f[2 * e + 1] = v.y;
       }
-      if constexpr (!QUANT) {
+    };
+    if constexpr (!QUANT) {
+      if constexpr (!VEC) group_barrier<TPR>(group);  // the slot is read: y takes its place
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        float f[E];
+        affine(i, f);
         if (live) write_vec<T, TPR, VEC>(y, buf, yof, C, l, i, f);
-      } else {
-        // 16 neighbouring threads hold 128 columns: one block
-        const int c = col_of<T, TPR>(l, i);
-        uint32_t a = 0;
-        if (c < C) {
+      }
+    } else {
+      // 16 neighbouring threads hold 128 columns: one block per vector. The blocks' maxima go
+      // through their shuffles together, so that the chains overlap.
+      float f[VPL][E];
+      uint32_t a[VPL], all = 0;
 #pragma unroll
-          for (int e = 0; e < E; ++e) a = max(a, abs_bits(f[e]));
+      for (int i = 0; i < VPL; ++i) {
+        affine(i, f[i]);
+        a[i] = 0;
+        if (col_of<T, TPR>(l, i) < C) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) a[i] = max(a[i], abs_bits(f[i][e]));
         }
+        all = max(all, a[i]);
+      }
+      if (__any_sync(0xffffffffu, all >= kInfBits)) {  // rare
 #pragma unroll
-        for (int o = 8; o; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-        if (__any_sync(0xffffffffu, a >= kInfBits)) {
-          a = 0;
-          if (c < C) {
+        for (int i = 0; i < VPL; ++i) {
+          a[i] = 0;
 #pragma unroll
-            for (int e = 0; e < E; ++e) a = max(a, finite_abs_bits(f[e]));
+          for (int e = 0; e < E; ++e) {
+            if (col_of<T, TPR>(l, i) < C) a[i] = max(a[i], finite_abs_bits(f[i][e]));
+            f[i][e] = inf_to_nan(f[i][e]);
           }
-#pragma unroll
-          for (int o = 8; o; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-#pragma unroll
-          for (int e = 0; e < E; ++e) f[e] = inf_to_nan(f[e]);
         }
-        const uint32_t byte = e8m0_byte(a);
+      }
+#pragma unroll
+      for (int o = 8; o; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) a[i] = max(a[i], __shfl_xor_sync(0xffffffffu, a[i], o));
+      uint8_t* q = p.q + static_cast<int64_t>(row) * p.ldq;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const int c = col_of<T, TPR>(l, i);
+        const uint32_t byte = e8m0_byte(a[i]);
         const float inv = e8m0_inverse(byte);
         if (live && c < C) {
           uint2 o;
-          o.x = e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-          o.y = e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
-          *reinterpret_cast<uint2*>(p.q + static_cast<int64_t>(row) * p.ldq + c) = o;
+          o.x = e4m3x4(f[i][0] * inv, f[i][1] * inv, f[i][2] * inv, f[i][3] * inv);
+          o.y = e4m3x4(f[i][4] * inv, f[i][5] * inv, f[i][6] * inv, f[i][7] * inv);
+          *reinterpret_cast<uint2*>(q + c) = o;
           if ((l & 15) == 0) p.scales[scale_offset(row, c >> 7, p.kq)] = static_cast<uint8_t>(byte);
         }
       }
