@@ -421,44 +421,45 @@ __global__ void __launch_bounds__(fwd_threads(TPR), TPR <= 256 ? 2 : 1)
     } else {
       // 16 neighbouring threads hold 128 columns: one block per vector. The blocks' maxima go
       // through their shuffles together, so that the chains overlap.
-      float f[VPL][E];
-      uint32_t a[VPL], all = 0;
+      float f[VPL][E], a[VPL], all = 0.f;  // maxima of magnitudes, which NaN does not enter
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
         affine(i, f[i]);
-        a[i] = 0;
+        a[i] = 0.f;
         if (col_of<T, TPR>(l, i) < C) {
 #pragma unroll
-          for (int e = 0; e < E; ++e) a[i] = max(a[i], abs_bits(f[i][e]));
+          for (int e = 0; e < E; ++e) a[i] = fmaxf(a[i], fabsf(f[i][e]));
         }
-        all = max(all, a[i]);
+        all = fmaxf(all, a[i]);
       }
-      if (__any_sync(0xffffffffu, all >= kInfBits)) {  // rare
+      if (__any_sync(0xffffffffu, abs_bits(all) >= kInfBits)) {  // rare: infinities
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-          a[i] = 0;
+          a[i] = 0.f;
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            if (col_of<T, TPR>(l, i) < C) a[i] = max(a[i], finite_abs_bits(f[i][e]));
             f[i][e] = inf_to_nan(f[i][e]);
+            if (col_of<T, TPR>(l, i) < C) a[i] = fmaxf(a[i], fabsf(f[i][e]));
           }
         }
       }
 #pragma unroll
       for (int o = 8; o; o >>= 1)
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) a[i] = max(a[i], __shfl_xor_sync(0xffffffffu, a[i], o));
+        for (int i = 0; i < VPL; ++i) a[i] = fmaxf(a[i], __shfl_xor_sync(0xffffffffu, a[i], o));
       uint8_t* q = p.q + static_cast<int64_t>(row) * p.ldq;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
         const int c = col_of<T, TPR>(l, i);
-        const uint32_t byte = e8m0_byte(a[i]);
+        const uint32_t byte = e8m0_byte(__float_as_uint(a[i]));
         const float inv = e8m0_inverse(byte);
+        const uint64_t inv2 = f2pack(inv, inv);
         if (live && c < C) {
-          uint2 o;
-          o.x = e4m3x4(f[i][0] * inv, f[i][1] * inv, f[i][2] * inv, f[i][3] * inv);
-          o.y = e4m3x4(f[i][4] * inv, f[i][5] * inv, f[i][6] * inv, f[i][7] * inv);
-          *reinterpret_cast<uint2*>(q + c) = o;
+          float2 g[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) g[e] = f2unpack(mul2(f2pack(f[i][2 * e], f[i][2 * e + 1]), inv2));
+          *reinterpret_cast<uint2*>(q + c) = make_uint2(e4m3x4(g[0].x, g[0].y, g[1].x, g[1].y),
+                                                        e4m3x4(g[2].x, g[2].y, g[3].x, g[3].y));
           if ((l & 15) == 0) p.scales[scale_offset(row, c >> 7, p.kq)] = static_cast<uint8_t>(byte);
         }
       }

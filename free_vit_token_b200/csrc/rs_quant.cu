@@ -44,17 +44,22 @@ struct Cols8 {  // bf16, fp16
       if (((w[i] >> 16) & 0x7FFFu) == kInf) w[i] |= 0x7FFF0000u;
     }
   }
-  // a word of magnitudes (of one column or two) as fp32 bits: the larger, or each half
+  // a 16-bit magnitude as fp32 bits; the one of a word's column e
   static __device__ __forceinline__ uint32_t wide(uint32_t h) {
     if constexpr (Elem<T>::kBf16) return h << 16;
     return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(h))));
   }
-  static __device__ __forceinline__ uint32_t top(uint32_t m) { return wide(max(m & 0xFFFFu, m >> 16)); }
   static __device__ __forceinline__ uint32_t col(uint32_t m, int e) { return wide(e ? m >> 16 : m & 0xFFFFu); }
-  __device__ __forceinline__ float get(int e) const {
-    const uint32_t v = w[e >> 1];
-    if constexpr (Elem<T>::kBf16) return (e & 1) ? bf16hi(v) : bf16lo(v);
-    return __half2float(__ushort_as_half(static_cast<unsigned short>((e & 1) ? v >> 16 : v & 0xFFFFu)));
+  __device__ __forceinline__ void pairs(uint64_t (&f)[4]) const {
+    Elem<T>::pairs(make_uint4(w[0], w[1], w[2], w[3]), f);
+  }
+  // the larger magnitudes of two rows, reduced over the 16 threads of a block: fp32 bits
+  static __device__ __forceinline__ void rows_top(uint32_t m0, uint32_t m1, uint32_t& t0, uint32_t& t1) {
+    uint32_t m = __vmaxu2(__byte_perm(m0, m1, 0x5410), __byte_perm(m0, m1, 0x7632));
+#pragma unroll
+    for (int o = 8; o; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    t0 = wide(m & 0xFFFFu);
+    t1 = wide(m >> 16);
   }
 };
 template <>
@@ -70,9 +75,20 @@ struct Cols8<float> {
     for (int i = 0; i < W; ++i)
       if ((w[i] & 0x7FFFFFFFu) == kInfBits) w[i] = 0x7FFFFFFFu;
   }
-  static __device__ __forceinline__ uint32_t top(uint32_t m) { return m; }
   static __device__ __forceinline__ uint32_t col(uint32_t m, int) { return m; }
-  __device__ __forceinline__ float get(int e) const { return __uint_as_float(w[e]); }
+  __device__ __forceinline__ void pairs(uint64_t (&f)[4]) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = (static_cast<uint64_t>(w[2 * e + 1]) << 32) | w[2 * e];
+  }
+  static __device__ __forceinline__ void rows_top(uint32_t m0, uint32_t m1, uint32_t& t0, uint32_t& t1) {
+    t0 = m0;
+    t1 = m1;
+#pragma unroll
+    for (int o = 8; o; o >>= 1) {
+      t0 = max(t0, __shfl_xor_sync(0xffffffffu, t0, o));
+      t1 = max(t1, __shfl_xor_sync(0xffffffffu, t1, o));
+    }
+  }
 };
 
 // Zero past K (and for rows that do not exist).
@@ -110,7 +126,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2) quantize_kernel(c
   constexpr int CW = 8 / V::W;  // columns of a word
   __shared__ __align__(16) uint8_t s_t[COLS ? kQTile * kQTile : 16];
   __shared__ uint32_t s_max[COLS ? 8 : 1][COLS ? kQTile / CW : 1];
-  __shared__ uint32_t s_byte[COLS ? kQTile : 1];
+  __shared__ __align__(8) float s_inv[COLS ? kQTile : 1];
   __shared__ float s_sum[COLS ? 8 : 1][COLS ? kQTile : 1];
   pdl_trigger();
   pdl_wait();
@@ -120,13 +136,16 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2) quantize_kernel(c
   const int row_tiles = (p.rows + kQTile - 1) / kQTile;
   const int kq = (p.K + 511) / 512, kqt = (p.rows + 511) / 512;
   const T* x = static_cast<const T*>(p.x);
-  float sum[8] = {};
+  uint64_t sum[4] = {};  // pairs of column sums
   V v[8], nx[8];
   auto load = [&](int rt, V (&d)[8]) {
     const int r0 = rt * kQTile + 8 * ty;
+    const T* row = x + static_cast<int64_t>(r0) * p.ldx;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      load8<T, VEC>(x + static_cast<int64_t>(r0 + j) * p.ldx, c, p.K, r0 + j < p.rows, d[j]);
+    for (int j = 0; j < 8; ++j) {
+      load8<T, VEC>(row, c, p.K, r0 + j < p.rows, d[j]);
+      row += p.ldx;
+    }
   };
   int rt = blockIdx.y;
   if (rt < row_tiles) load(rt, v);
@@ -147,9 +166,16 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2) quantize_kernel(c
         if constexpr (COLS) cm[i] = V::vmax(cm[i], m);
       }
       all = V::vmax(all, rm[j]);
-      if constexpr (COLS) {
+    }
+    if constexpr (COLS) {
+      if (p.partials != nullptr) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] += v[j].get(e);
+        for (int j = 0; j < 8; ++j) {
+          uint64_t f[4];
+          v[j].pairs(f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[e] = fadd2(sum[e], f[e]);
+        }
       }
     }
     if (V::nonfinite(all)) {  // rare: infinities become NaN, and neither counts
@@ -180,38 +206,66 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2) quantize_kernel(c
 #pragma unroll
         for (int w = 1; w < 8; ++w) m = V::vmax(m, s_max[w][t / CW]);
         const uint32_t byte = e8m0_byte(V::col(m, t % CW));
-        s_byte[t] = byte;
+        s_inv[t] = e8m0_inverse(byte);
         if (c0 + t < p.K) p.scales_t[scale_offset(c0 + t, rt, kqt)] = static_cast<uint8_t>(byte);
       }
     }
+    uint32_t byte[8];
     if constexpr (ROWS) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        uint32_t m = rm[j];
+      for (int j = 0; j < 8; j += 2) {
+        uint32_t a, b;
+        V::rows_top(rm[j], rm[j + 1], a, b);
+        byte[j] = e8m0_byte(a);
+        byte[j + 1] = e8m0_byte(b);
+      }
+      if (tx == 0) {  // 8 rows of one group of 32: their bytes are 16 apart
+        uint8_t* sc = p.scales + scale_offset(r0, c0 >> 7, kq);
 #pragma unroll
-        for (int o = 8; o; o >>= 1) m = V::vmax(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const uint32_t byte = e8m0_byte(V::top(m));
-        const float inv = e8m0_inverse(byte);
-        const int r = r0 + j;
-        if (r < p.rows && c < p.K) {
-          uint2 o;
-          o.x = e4m3x4(v[j].get(0) * inv, v[j].get(1) * inv, v[j].get(2) * inv, v[j].get(3) * inv);
-          o.y = e4m3x4(v[j].get(4) * inv, v[j].get(5) * inv, v[j].get(6) * inv, v[j].get(7) * inv);
-          *reinterpret_cast<uint2*>(p.q + static_cast<int64_t>(r) * p.ldq + c) = o;
-          if (tx == 0) p.scales[scale_offset(r, c0 >> 7, kq)] = static_cast<uint8_t>(byte);
+        for (int j = 0; j < 8; ++j)
+          if (r0 + j < p.rows) sc[16 * j] = static_cast<uint8_t>(byte[j]);
+      }
+    }
+    uint64_t inv[4] = {};  // pairs of column factors
+    if constexpr (COLS) {
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        inv[e] = *reinterpret_cast<const uint64_t*>(s_inv + 8 * tx + 2 * e);
+    }
+    uint8_t* q = p.q + static_cast<int64_t>(r0) * p.ldq + c;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // four rows at a time
+      uint64_t f[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[4 * h + j].pairs(f[j]);
+      if constexpr (ROWS) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float ri = e8m0_inverse(byte[4 * h + j]);
+          const uint64_t r2 = f2pack(ri, ri);
+          float2 g[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) g[e] = f2unpack(mul2(f[j][e], r2));
+          if (r0 + 4 * h + j < p.rows && c < p.K)
+            *reinterpret_cast<uint2*>(q) = make_uint2(e4m3x4(g[0].x, g[0].y, g[1].x, g[1].y),
+                                                      e4m3x4(g[2].x, g[2].y, g[3].x, g[3].y));
+          q += p.ldq;
+        }
+      }
+      if constexpr (COLS) {
+        uint8_t* d = s_t + 8 * tx * kQTile + ((ty ^ tx) << 3) + 4 * h;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float2 g[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) g[j] = f2unpack(mul2(f[j][e], inv[e]));
+          *reinterpret_cast<uint32_t*>(d + 2 * e * kQTile) = e4m3x4(g[0].x, g[1].x, g[2].x, g[3].x);
+          *reinterpret_cast<uint32_t*>(d + (2 * e + 1) * kQTile) = e4m3x4(g[0].y, g[1].y, g[2].y, g[3].y);
         }
       }
     }
     if constexpr (COLS) {
-      __syncthreads();
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float inv = e8m0_inverse(s_byte[8 * tx + e]);
-        uint2 o;
-        o.x = e4m3x4(v[0].get(e) * inv, v[1].get(e) * inv, v[2].get(e) * inv, v[3].get(e) * inv);
-        o.y = e4m3x4(v[4].get(e) * inv, v[5].get(e) * inv, v[6].get(e) * inv, v[7].get(e) * inv);
-        *reinterpret_cast<uint2*>(s_t + (8 * tx + e) * kQTile + ((ty ^ tx) << 3)) = o;
-      }
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -224,7 +278,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2) quantize_kernel(c
           *reinterpret_cast<uint4*>(p.qt + static_cast<int64_t>(c0 + col) * p.ldqt + r) = o;
       }
       // Three barriers a tile order the shared arrays: s_max is written before the first and
-      // read before the second, s_byte written before the second and read before the third,
+      // read before the second, s_inv written before the second and read before the third,
       // s_t written before the third and read before the next tile's first.
     }
 #pragma unroll
@@ -233,10 +287,14 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2) quantize_kernel(c
   if constexpr (COLS) {
     if (p.partials != nullptr) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 16);
-      if ((t & 16) == 0) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s_sum[warp][8 * tx + e] = sum[e];
+      for (int e = 0; e < 4; ++e) {
+        float2 a = f2unpack(sum[e]);
+        a.x += __shfl_xor_sync(0xffffffffu, a.x, 16);
+        a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
+        if ((t & 16) == 0) {
+          s_sum[warp][8 * tx + 2 * e] = a.x;
+          s_sum[warp][8 * tx + 2 * e + 1] = a.y;
+        }
       }
       __syncthreads();
       if (t < kQTile && c0 + t < p.K) {
