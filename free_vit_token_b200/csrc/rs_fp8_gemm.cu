@@ -23,35 +23,13 @@
 #include <cuda_runtime.h>
 
 #include "rs_fp8.cuh"
-#include "rs_gelu.cuh"
-#include "rs_gelu_logit.h"
+#include "rs_gelu8.cuh"
 #include "rs_ops.h"
 #include "rs_ptx_mx.cuh"
 
 namespace rs {
 
 namespace {
-
-// GELU of two fp32 lanes through a logistic form of the normal CDF (rs_gelu_logit.h, max
-// |error| 1.5e-5 with the approximate 2^x and reciprocal). Against the polynomials of
-// rs_gelu.cuh it takes half the FMAs, three instructions of the exponential unit a pair (one
-// reciprocal serves both lanes: 1/a = b / (ab)) and no choice by range: 50432 x 384 -> 1536 on
-// values past the short polynomial's range 92 -> 73 us a call.
-__device__ __forceinline__ uint64_t gelu2_logit(uint64_t z2) {
-  const float2 s = f2unpack(mul2(z2, z2));
-  const uint64_t t = f2pack(fminf(s.x, RS_GELU_LOGIT_T), fminf(s.y, RS_GELU_LOGIT_T));
-  uint64_t q = kpair(-RS_GELU_LOGIT_Q3);
-  q = ffma2(q, t, kpair(-RS_GELU_LOGIT_Q2));
-  q = ffma2(q, t, kpair(-RS_GELU_LOGIT_Q1));
-  q = ffma2(q, t, kpair(-RS_GELU_LOGIT_Q0));
-  const float2 x = f2unpack(mul2(q, z2));
-  // up to 2^60, so that the product of two stays finite (the CDF is below 1e-17 there)
-  const float2 d = f2unpack(
-      fadd2(f2pack(ex2_approx(fminf(x.x, 60.f)), ex2_approx(fminf(x.y, 60.f))), kpair(1.f)));
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d.x * d.y));
-  return mul2(z2, f2pack(r * d.y, r * d.x));
-}
 
 constexpr int kGM = 128;                       // rows of A per CTA and tile
 constexpr int kGK = 128;                       // K elements (bytes) per stage
@@ -593,6 +571,13 @@ int tmap_2d(CUtensorMap* m, CUtensorMapDataType t, int es, const void* base, uin
              : RS_ERR_CUDA;
 }
 
+}  // namespace
+
+int tmap_operand(CUtensorMap* m, const void* base, int K, int rows, int64_t ld, int box_rows) {
+  return tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, K, rows, ld, kGK, box_rows,
+                 CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 // Scale tiles as [row tiles][tiles along K][128 words].
 int tmap_scales(CUtensorMap* m, const void* base, int rows, int K, uint32_t tiles) {
   auto fn = encode_fn();
@@ -609,6 +594,8 @@ int tmap_scales(CUtensorMap* m, const void* base, int rows, int K, uint32_t tile
              : RS_ERR_CUDA;
 }
 
+namespace {
+
 template <int BN, bool PAIR, int OUT>
 int go(Fp8Gemm p, int num_sms, cudaStream_t s, bool pdl) {
   constexpr int tile_m = PAIR ? 256 : 128;
@@ -616,10 +603,8 @@ int go(Fp8Gemm p, int num_sms, cudaStream_t s, bool pdl) {
   p.num_tiles = ((p.M + tile_m - 1) / tile_m) * p.n_blocks;
   CUtensorMap tA, tB, tSA, tSB, tO{};
   const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  int st = tmap_2d(&tA, u8, 1, p.a, p.K, p.M, p.lda, kGK, kGM, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (st == RS_OK)
-    st = tmap_2d(&tB, u8, 1, p.b, p.K, p.N, p.ldb, kGK, PAIR ? BN / 2 : BN,
-                 CU_TENSOR_MAP_SWIZZLE_128B);
+  int st = tmap_operand(&tA, p.a, p.K, p.M, p.lda, kGM);
+  if (st == RS_OK) st = tmap_operand(&tB, p.b, p.K, p.N, p.ldb, PAIR ? BN / 2 : BN);
   if (st == RS_OK) st = tmap_scales(&tSA, p.sa, p.M, p.K, 1);
   if (st == RS_OK) st = tmap_scales(&tSB, p.sb, p.N, p.K, g_scale_tiles_b(BN));
   constexpr int es = OUT == kOutQ8 ? 1 : OUT == kOutBf16 ? 2 : 4;

@@ -304,7 +304,8 @@ int rs_fp8_gemm(const void* a, int64_t lda, const void* scales_a, const void* b,
 }
 
 uint64_t rs_fp8_linear_ws_bytes(int M, int K) {
-  return M < 0 || M >= kMaxDim || !dim_ok(K) ? 0 : q_space(M > 0 ? M : 1, K).bytes;
+  if (M < 0 || M >= kMaxDim || !dim_ok(K) || rs::fp8_few_rows(M, K)) return 0;
+  return q_space(M, K).bytes;
 }
 
 int rs_fp8_linear(const void* x, int64_t ldx, int M, int K, int N, const void* wq, int64_t ldw,
@@ -317,8 +318,30 @@ int rs_fp8_linear(const void* x, int64_t ldx, int M, int K, int N, const void* w
   if (!x || !out) return RS_ERR_NULL;
   if (!aligned(x, 2) || !aligned(out, 2)) return RS_ERR_ALIGN;
   RS_TRY(check_q(wq, ldw, scales_w, K));
-  RS_TRY(check_ws(ws, ws_bytes, rs_fp8_linear_ws_bytes(M, K)));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rs::fp8_few_rows(M, K)) {
+    rs::Fp8Few f{};
+    f.x = static_cast<const __nv_bfloat16*>(x);
+    f.ldx = ldx;
+    f.xvec = aligned(x, 16) && ldx % 8 == 0;
+    f.M = M;
+    f.N = N;
+    f.K = K;
+    f.w = wq;
+    f.ldw = ldw;
+    f.sw = scales_w;
+    f.bias = static_cast<const __nv_bfloat16*>(bias);
+    f.gelu = gelu;
+    f.resid = static_cast<const __nv_bfloat16*>(resid);
+    f.ldr = ldr;
+    f.out = static_cast<__nv_bfloat16*>(out);
+    f.ldo = ldo;
+    f.timeout_ns = rs::kDefaultTimeoutNs;
+    int sms = 0;
+    RS_TRY(rs::device_flag(&sms, &f.err));
+    return rs::launch_fp8_few(f, sms, s);
+  }
+  RS_TRY(check_ws(ws, ws_bytes, rs_fp8_linear_ws_bytes(M, K)));
   const QSpace w = q_space(M, K);
   rs::Quant qp{};
   qp.x = x;

@@ -107,4 +107,31 @@ struct Fp8Gemm {
 // RS_OK or an error status.
 int launch_fp8_gemm(const Fp8Gemm& p, int out, int num_sms, cudaStream_t s, bool pdl = false);
 
+// Tensor maps of a quantised operand [rows][ld] (128-byte swizzled boxes of 128 K x box_rows)
+// and of its scale tiles as [row tiles][tiles along K][128 words] in boxes of `tiles` row tiles.
+int tmap_operand(CUtensorMap* m, const void* base, int K, int rows, int64_t ld, int box_rows);
+int tmap_scales(CUtensorMap* m, const void* base, int rows, int K, uint32_t tiles);
+
+// A linear layer on a few rows (rs_fp8_few.cu): quantisation and product in one launch.
+struct Fp8Few {
+  const __nv_bfloat16* x;     // [M][ldx]
+  int64_t ldx;
+  int xvec;                   // x's rows start on 16 bytes
+  int M, N, K;
+  const void* w;              // [N][ldw] e4m3
+  int64_t ldw;
+  const void* sw;
+  const __nv_bfloat16* bias;  // [N] or null
+  int gelu;
+  const __nv_bfloat16* resid; // [M][ldr] or null
+  int64_t ldr;
+  __nv_bfloat16* out;         // [M][ldo]
+  int64_t ldo;
+  int* err;
+  unsigned long long timeout_ns;
+  int split, blocks;          // set by the launcher: CTAs per reduction, K blocks of each
+};
+bool fp8_few_rows(int M, int K);  // does launch_fp8_few take these sizes?
+int launch_fp8_few(Fp8Few p, int num_sms, cudaStream_t s);
+
 }  // namespace rs

@@ -590,6 +590,8 @@ def _ws(ws: Optional[torch.Tensor], device: torch.device, dev: int, name: str, *
     (the tensor must live until the call is queued). `name` is the size function."""
     if ws is None:
         n = _ws_size(name, *sizes)
+        if n == 0:  # none needed (or sizes that the call will refuse)
+            return None, 0, None
         ws = torch.empty(n, dtype=torch.uint8, device=device)
         return ws.data_ptr() or None, n, ws
     if not ws.is_contiguous():

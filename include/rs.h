@@ -390,8 +390,8 @@ int rs_debug_fc1_skip_load(const void* x, int M, int C, int H, const void* W1, c
  *     alignment of their element type only, unless stated; rows that all start on 16 bytes
  *     and are a whole number of 16-byte vectors run fastest.
  *   - There is no library workspace: calls that need scratch take `ws` (256-byte aligned) and
- *     `ws_bytes`, at least what the matching _ws_bytes function says (0 if the sizes are
- *     invalid). Scratch holds nothing between calls, so calls with their own scratch may
+ *     `ws_bytes`, at least what the matching _ws_bytes function says (0 where a call needs
+ *     none, ws may then be NULL, or the sizes are invalid). Scratch holds nothing between calls, so calls with their own scratch may
  *     overlap on any streams and be captured into any graphs.
  *   - 0 <= rows < 2^27; other sizes as stated. Without rows nothing is launched except what
  *     sets gradient sums to zero.
@@ -464,7 +464,8 @@ int rs_fp8_gemm(const void* a, int64_t lda, const void* scales_a, const void* b,
 
 /* A linear layer with its weight held in 8 bits: x [M, K] bf16 is quantised along K, then
  * out [M, N] bf16 = act(x W^T + bias) + resid as rs_fp8_gemm. wq [N, ldw], scales_w: W [N, K]
- * in 8-bit blocks. */
+ * in 8-bit blocks. Up to 32 rows with K <= 8192 run as one launch without scratch, the
+ * reduction split over a cluster of CTAs; more as rs_fp8_quantize and rs_fp8_gemm. */
 int rs_fp8_linear(const void* x, int64_t ldx, int M, int K, int N, const void* wq, int64_t ldw,
                   const void* scales_w, const void* bias, int gelu, const void* resid, int64_t ldr,
                   void* out, int64_t ldo, void* ws, uint64_t ws_bytes, void* stream);

@@ -208,6 +208,8 @@ def test_gemm_unwritten_scale_bytes_do_not_matter():
 
 # ------------------------------------------------------------------ linear layer
 @pytest.mark.parametrize("M,N,K", [(1, 4096, 1024), (2, 100, 100), (15, 77, 333), (16, 8192, 2048),
+                                   (1, 1, 1), (1, 129, 8192), (3, 64, 8000), (17, 300, 1100),
+                                   (32, 4096, 640), (31, 1000, 5000), (32, 20000, 128), (9, 520, 8193),
                                    (33, 512, 64), (100, 1536, 384), (1569, 1024, 1000)])
 def test_linear(M, N, K):
     rs = _rs()
@@ -436,6 +438,6 @@ def test_refusals():
     with pytest.raises(ValueError):
         rs.rs_fp8_quantize(torch.zeros(4, 64, device=dev), colsum=True)
     with pytest.raises(rs.RsError):
-        rs.rs_fp8_linear(torch.zeros(4, 64, dtype=BF, device=dev), b,
+        rs.rs_fp8_linear(torch.zeros(40, 64, dtype=BF, device=dev), b,
                          ws=torch.empty(256, dtype=torch.uint8, device=dev))
     assert rs.rs_get_last_device_error() == 0

@@ -86,7 +86,7 @@ def test_gemm(kw, want):
     assert gemm(**kw) == want
 
 
-def linear(x=F, ldx=200, M=4, K=200, N=24, w=F, ldw=208, sw=F, bias=F, gelu=0, r=None, ldr=24, o=F,
+def linear(x=F, ldx=200, M=40, K=200, N=24, w=F, ldw=208, sw=F, bias=F, gelu=0, r=None, ldr=24, o=F,
            ldo=24, ws=F, n=BIG):
     return rs.lib().rs_fp8_linear(x, ldx, M, K, N, w, ldw, sw, bias, gelu, r, ldr, o, ldo, ws, n, None)
 
@@ -132,7 +132,8 @@ def test_sizes():
     L = rs.lib()
     assert L.rs_fp8_scale_bytes(1, 1) == 512 and L.rs_fp8_scale_bytes(129, 513) == 2048
     assert L.rs_fp8_scale_bytes(0, 64) == 0 and L.rs_fp8_scale_bytes(4, 0) == 0
-    assert L.rs_fp8_linear_ws_bytes(3, 200) >= 3 * 208 + 512
+    assert L.rs_fp8_linear_ws_bytes(33, 200) >= 33 * 208 + 512
+    assert L.rs_fp8_linear_ws_bytes(32, 8192) == 0 and L.rs_fp8_linear_ws_bytes(32, 8193) > 0
     assert L.rs_fp8_quantize_ws_bytes(129, 200) >= 2 * 200 * 4
     assert L.rs_fp8_linear_backward_ws_bytes(130, 24) >= 130 * 32 + 24 * 144 + 2 * 24 * 4
     assert L.rs_mlp_forward_fp8_ws_bytes(10, 64, 128) >= 10 * 192
