@@ -618,8 +618,8 @@ int go(Fp8Gemm p, int num_sms, cudaStream_t s, bool pdl) {
   if (st != RS_OK) return st;
   auto kern = fp8_gemm_kernel<BN, PAIR, OUT>;
   constexpr size_t smem = g_smem(BN, PAIR);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess) {
+  static std::atomic<uint64_t> allowed{0};
+  if (allow_smem(kern, static_cast<int>(smem), allowed) != cudaSuccess) {
     cudaGetLastError();
     return RS_ERR_CUDA;
   }

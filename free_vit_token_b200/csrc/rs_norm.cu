@@ -672,7 +672,8 @@ static cudaError_t go_fwd_p(const LnForward& p, int num_sms, cudaStream_t s) {
   constexpr int per_sm = TPR <= 256 && 2 * (smem + 2048) <= 232448 ? 2 : 1;
   auto kern = ln_fwd_kernel<T, TPR, VPL, VEC, P32, QUANT>;
   if constexpr (smem > 40 * 1024) {  // with the static part past the default 48 KB
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(kern, smem, allowed);
     if (e != cudaSuccess) return e;
   }
   const int blocks = (p.M + groups - 1) / groups, most = per_sm * num_sms;
@@ -736,8 +737,8 @@ static cudaError_t go_bwd_p(const LnBackward& p, int num_sms, int* P, cudaStream
   static_assert(smem + 1024 <= 232448, "shared memory");
   auto kern = ln_bwd_kernel<T, TPR, VPL, VEC, P32>;
   if constexpr (smem > 40 * 1024) {  // with the static part past the default 48 KB
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(kern, static_cast<int>(smem), allowed);
     if (e != cudaSuccess) return e;
   }
   const int64_t blocks = (static_cast<int64_t>(p.M) + threads / TPR - 1) / (threads / TPR);

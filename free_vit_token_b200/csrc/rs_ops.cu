@@ -304,7 +304,7 @@ int rs_fp8_gemm(const void* a, int64_t lda, const void* scales_a, const void* b,
 }
 
 uint64_t rs_fp8_linear_ws_bytes(int M, int K) {
-  if (M < 0 || M >= kMaxDim || !dim_ok(K) || rs::fp8_few_rows(M, K)) return 0;
+  if (M < 0 || M >= kMaxDim || !dim_ok(K) || rs::fp8_few_rows(M, 1 << 26, K)) return 0;
   return q_space(M, K).bytes;
 }
 
@@ -319,7 +319,7 @@ int rs_fp8_linear(const void* x, int64_t ldx, int M, int K, int N, const void* w
   if (!aligned(x, 2) || !aligned(out, 2)) return RS_ERR_ALIGN;
   RS_TRY(check_q(wq, ldw, scales_w, K));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (rs::fp8_few_rows(M, K)) {
+  if (rs::fp8_few_rows(M, N, K)) {
     rs::Fp8Few f{};
     f.x = static_cast<const __nv_bfloat16*>(x);
     f.ldx = ldx;

@@ -2,6 +2,8 @@
 // parameter blocks and host-side launchers). Not part of the C ABI.
 #pragma once
 
+#include <atomic>
+
 #include "rs_internal.h"
 
 namespace rs {
@@ -10,6 +12,19 @@ namespace rs {
 // device's first use): RS_OK or an error. Defined beside the library's device state.
 int device_sms(int* num_sms);
 int device_flag(int* num_sms, int** err);
+// Allows `kern` `bytes` of dynamic shared memory on the current device, once per device (`done`
+// is the kernel's own, one bit per device): the call costs as much as a third of a launch.
+template <typename... A>
+inline cudaError_t allow_smem(void (*kern)(A...), int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // Layer norm forward (rs_norm.cu): y (or q and scales, by launcher) and optional row stats.
 struct LnForward {
@@ -131,7 +146,7 @@ struct Fp8Few {
   unsigned long long timeout_ns;
   int split, blocks;          // set by the launcher: CTAs per reduction, K blocks of each
 };
-bool fp8_few_rows(int M, int K);  // does launch_fp8_few take these sizes?
+bool fp8_few_rows(int M, int N, int K);  // does rs_fp8_linear take this path?
 int launch_fp8_few(Fp8Few p, int num_sms, cudaStream_t s);
 
 }  // namespace rs

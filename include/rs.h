@@ -464,8 +464,9 @@ int rs_fp8_gemm(const void* a, int64_t lda, const void* scales_a, const void* b,
 
 /* A linear layer with its weight held in 8 bits: x [M, K] bf16 is quantised along K, then
  * out [M, N] bf16 = act(x W^T + bias) + resid as rs_fp8_gemm. wq [N, ldw], scales_w: W [N, K]
- * in 8-bit blocks. Up to 32 rows with K <= 8192 run as one launch without scratch, the
- * reduction split over a cluster of CTAs; more as rs_fp8_quantize and rs_fp8_gemm. */
+ * in 8-bit blocks. A few rows (up to 16, or 32 for N <= 8192, with K <= 8192) run as one launch,
+ * the reduction split over a cluster of CTAs, others as rs_fp8_quantize and rs_fp8_gemm. Up to
+ * 16 rows with K <= 8192 need no scratch. */
 int rs_fp8_linear(const void* x, int64_t ldx, int M, int K, int N, const void* wq, int64_t ldw,
                   const void* scales_w, const void* bias, int gelu, const void* resid, int64_t ldr,
                   void* out, int64_t ldo, void* ws, uint64_t ws_bytes, void* stream);

@@ -133,7 +133,8 @@ def test_sizes():
     assert L.rs_fp8_scale_bytes(1, 1) == 512 and L.rs_fp8_scale_bytes(129, 513) == 2048
     assert L.rs_fp8_scale_bytes(0, 64) == 0 and L.rs_fp8_scale_bytes(4, 0) == 0
     assert L.rs_fp8_linear_ws_bytes(33, 200) >= 33 * 208 + 512
-    assert L.rs_fp8_linear_ws_bytes(32, 8192) == 0 and L.rs_fp8_linear_ws_bytes(32, 8193) > 0
+    assert L.rs_fp8_linear_ws_bytes(16, 8192) == 0 and L.rs_fp8_linear_ws_bytes(16, 8193) > 0
+    assert L.rs_fp8_linear_ws_bytes(17, 8192) > 0
     assert L.rs_fp8_quantize_ws_bytes(129, 200) >= 2 * 200 * 4
     assert L.rs_fp8_linear_backward_ws_bytes(130, 24) >= 130 * 32 + 24 * 144 + 2 * 24 * 4
     assert L.rs_mlp_forward_fp8_ws_bytes(10, 64, 128) >= 10 * 192
