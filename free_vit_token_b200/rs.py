@@ -615,6 +615,15 @@ def _matrix(x: torch.Tensor, M: int, N: int, dtype: torch.dtype) -> torch.Tensor
     return torch.empty(*x.shape[:-1], N, dtype=dtype, device=x.device)
 
 
+def _on(stream, fn, *args, **kwargs):
+    """fn(*args, **kwargs) with `stream` as the current one: what the call allocates, scratch
+    above all, then belongs to the stream that uses it."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return fn(*args, **kwargs)
+
+
 def _scale_bytes(rows: int, K: int) -> int:
     return (rows + 127) // 128 * ((K + 511) // 512) * 512
 
@@ -644,6 +653,8 @@ def rs_ln_forward(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
                   stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """x [..., C] (bf16, fp16 or fp32; a matrix may have strided rows) -> (LN(x) of the same
     type, stats [M, 2] fp32 with each row's mean and 1/std for rs_ln_backward). y may be x."""
+    if stream is not None:
+        return _on(stream, rs_ln_forward, x, gamma, beta, eps, y, stats)
     dev, dt = _device(x, "x"), _float_type(x)
     px, ldx, M = _rows(x, "x", dev)
     C = x.shape[-1]
@@ -658,7 +669,7 @@ def rs_ln_forward(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
         ps = stats.data_ptr() or None
     else:
         ps = _vec(stats, "stats", dev, 2 * M, torch.float32)
-    _check(lib().rs_ln_forward(px, ldx, M, C, dt, pg, pb, pdt, eps, py, ldy, ps, _stream(stream)),
+    _check(lib().rs_ln_forward(px, ldx, M, C, dt, pg, pb, pdt, eps, py, ldy, ps, _stream(None)),
            "rs_ln_forward")
     return y, stats
 
@@ -669,6 +680,8 @@ def rs_ln_quantize(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
                    stream=None) -> Fp8:
     """LN(x) in 8-bit blocks along C (x bf16 or fp16, C a multiple of 8); `stats` [M, 2] fp32
     also receives each row's mean and 1/std."""
+    if stream is not None:
+        return _on(stream, rs_ln_quantize, x, gamma, beta, eps, out, stats)
     dev, dt = _device(x, "x"), _float_type(x)
     px, ldx, M = _rows(x, "x", dev)
     C = x.shape[-1]
@@ -677,7 +690,7 @@ def rs_ln_quantize(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
         out = _fp8_empty(M, C, x.device)
     q, ldq, sc = _fp8(out, "out", dev, M, C)
     _check(lib().rs_ln_quantize(px, ldx, M, C, dt, pg, pb, pdt, eps, q, ldq, sc,
-                                _vec(stats, "stats", dev, 2 * M, torch.float32), _stream(stream)),
+                                _vec(stats, "stats", dev, 2 * M, torch.float32), _stream(None)),
            "rs_ln_quantize")
     return out
 
@@ -689,6 +702,8 @@ def rs_ln_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor,
                    stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """Gradients of y = LN(x) for dy: (dx, of x's type, with `dres` added; dgamma [C] fp32;
     dbeta [C] fp32). `stats` as rs_ln_forward returned them; dx may be dres."""
+    if stream is not None:
+        return _on(stream, rs_ln_backward, dy, x, stats, gamma, dres, dx, dgamma, dbeta, ws)
     dev, dt = _device(x, "x"), _float_type(x)
     px, ldx, M = _rows(x, "x", dev)
     C, device, f32 = x.shape[-1], x.device, torch.float32
@@ -707,7 +722,7 @@ def rs_ln_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor,
     pw, nw, ws = _ws(ws, device, dev, "rs_ln_backward_ws_bytes", M, C)
     st = lib().rs_ln_backward(pdy, lddy, px, ldx, pdr, lddr, _vec(stats, "stats", dev, 2 * M, f32),
                               pg, pdt, M, C, dt, pdx, lddx, _vec(dgamma, "dgamma", dev, C, f32),
-                              _vec(dbeta, "dbeta", dev, C, f32), pw, nw, _stream(stream))
+                              _vec(dbeta, "dbeta", dev, C, f32), pw, nw, _stream(None))
     _check(st, "rs_ln_backward")
     return dx, dgamma, dbeta
 
@@ -722,6 +737,8 @@ def rs_fp8_quantize(x: torch.Tensor, rows: bool = True, cols: bool = False, cols
     """x [M, K] (bf16, fp16 or fp32) to 8-bit blocks of 128 along K (`rows`), and/or its
     transpose [K, M] in blocks along M (`cols`), and/or its column sums [K] fp32 (`colsum`,
     needs cols), from one read: a triple, None for what was not asked for."""
+    if stream is not None:
+        return _on(stream, rs_fp8_quantize, x, rows, cols, colsum, out, out_t)
     dev, dt = _device(x, "x"), _float_type(x)
     px, ldx, M = _rows(x, "x", dev)
     K, device = x.shape[-1], x.device
@@ -742,7 +759,7 @@ def rs_fp8_quantize(x: torch.Tensor, rows: bool = True, cols: bool = False, cols
         ps = sums.data_ptr()
         pw, nw, ws = _ws(None, device, dev, "rs_fp8_quantize_ws_bytes", M, K)
     _check(lib().rs_fp8_quantize(px, ldx, M, K, dt, q, ldq, sc, qt, ldqt, sct, ps, pw, nw,
-                                 _stream(stream)), "rs_fp8_quantize")
+                                 _stream(None)), "rs_fp8_quantize")
     return out if rows else None, out_t if cols else None, sums
 
 
@@ -751,6 +768,8 @@ def rs_fp8_gemm(a: Fp8, b: Fp8, bias: Optional[torch.Tensor] = None, gelu: bool 
                 out_dtype: Optional[torch.dtype] = None, stream=None):
     """act(A B^T + bias) + resid of two quantised operands [M, K] and [N, K]: a bf16 (default)
     or fp32 tensor [M, N], or with out_dtype=torch.float8_e4m3fn an Fp8."""
+    if stream is not None:
+        return _on(stream, rs_fp8_gemm, a, b, bias, gelu, resid, out, out_dtype)
     M, N, K, device = a.rows, b.rows, a.K, a.q.device
     dev = _device(a.q, "a")
     pa, lda, sa = _fp8(a, "a", dev)
@@ -775,7 +794,7 @@ def rs_fp8_gemm(a: Fp8, b: Fp8, bias: Optional[torch.Tensor] = None, gelu: bool 
         pr, ldr, _ = _rows(resid, "resid", dev, out_dtype, N, M)
     _check(lib().rs_fp8_gemm(pa, lda, sa, pb, ldb, sb, M, N, K,
                              _vec(bias, "bias", dev, N, torch.bfloat16), int(gelu), pr, ldr, po,
-                             ldo, dt, so, _stream(stream)), "rs_fp8_gemm")
+                             ldo, dt, so, _stream(None)), "rs_fp8_gemm")
     return out
 
 
@@ -785,6 +804,8 @@ def rs_fp8_linear(x: torch.Tensor, w: Fp8, bias: Optional[torch.Tensor] = None,
                   stream=None) -> torch.Tensor:
     """x [..., K] bf16, quantised along K in the call, through a linear layer whose weight
     [N, K] is held in 8 bits: act(x W^T + bias) + resid [..., N] bf16."""
+    if stream is not None:
+        return _on(stream, rs_fp8_linear, x, w, bias, gelu, resid, out, ws)
     N, K, bf = w.rows, w.K, torch.bfloat16
     dev = _device(x, "x")
     px, ldx, M = _rows(x, "x", dev, bf, K)
@@ -797,7 +818,7 @@ def rs_fp8_linear(x: torch.Tensor, w: Fp8, bias: Optional[torch.Tensor] = None,
     pr, ldr = (None, N) if resid is None else _rows(resid, "resid", dev, bf, N, M)[:2]
     pws, nws, ws = _ws(ws, x.device, dev, "rs_fp8_linear_ws_bytes", M, K)
     _check(lib().rs_fp8_linear(px, ldx, M, K, N, pw, ldw, sw, _vec(bias, "bias", dev, N, bf),
-                               int(gelu), pr, ldr, po, ldo, pws, nws, _stream(stream)),
+                               int(gelu), pr, ldr, po, ldo, pws, nws, _stream(None)),
            "rs_fp8_linear")
     return out
 
@@ -809,6 +830,8 @@ def rs_fp8_linear_backward(dy: torch.Tensor, xt: Optional[Fp8], wt: Optional[Fp8
     operands (rs_fp8_quantize(..., cols=True)): xt of x, [K, M], and wt of W, [K, N]. Returns
     (dx [M, K] bf16, dw [N, K], db [N] fp32), None for dx without wt, dw without xt and db
     without `bias`."""
+    if stream is not None:
+        return _on(stream, rs_fp8_linear_backward, dy, xt, wt, bias, dw_dtype, ws)
     dev = _device(dy, "dy")
     pdy, lddy, M = _rows(dy, "dy", dev, torch.bfloat16)
     N, device = dy.shape[-1], dy.device
@@ -832,7 +855,7 @@ def rs_fp8_linear_backward(dy: torch.Tensor, xt: Optional[Fp8], wt: Optional[Fp8
         pdb = db.data_ptr()
     pws, nws, ws = _ws(ws, device, dev, "rs_fp8_linear_backward_ws_bytes", M, N)
     _check(lib().rs_fp8_linear_backward(pdy, lddy, M, N, K, px, ldx, sx, pw, ldw, sw, pdx, K, pdw,
-                                        K, _DTYPES[dw_dtype], pdb, pws, nws, _stream(stream)),
+                                        K, _DTYPES[dw_dtype], pdb, pws, nws, _stream(None)),
            "rs_fp8_linear_backward")
     return dx, dw, db
 
@@ -842,6 +865,8 @@ def rs_mlp_forward_fp8(x: torch.Tensor, w1: Fp8, b1, w2: Fp8, b2, gamma, beta,
                        stream=None) -> torch.Tensor:
     """rs_mlp_forward with W1 [H, C] and W2 [C, H] held in 8-bit blocks and both products in 8
     bits: x [..., C] bf16 -> x + MLP(LN(x)), same shape. out may be x."""
+    if stream is not None:
+        return _on(stream, rs_mlp_forward_fp8, x, w1, b1, w2, b2, gamma, beta, out, ws)
     C, H, bf = w1.K, w1.rows, torch.bfloat16
     dev = _device(x, "x")
     px, ldx, M = _rows(x, "x", dev, bf, C)
@@ -857,6 +882,6 @@ def rs_mlp_forward_fp8(x: torch.Tensor, w1: Fp8, b1, w2: Fp8, b2, gamma, beta,
     st = lib().rs_mlp_forward_fp8(px, M, C, H, p1, ld1, s1, _vec(b1, "b1", dev, H, bf), p2, ld2, s2,
                                   _vec(b2, "b2", dev, C, bf), _vec(gamma, "gamma", dev, C, bf),
                                   _vec(beta, "beta", dev, C, bf),
-                                  _rows(out, "out", dev, bf, C, M)[0], pws, nws, _stream(stream))
+                                  _rows(out, "out", dev, bf, C, M)[0], pws, nws, _stream(None))
     _check(st, "rs_mlp_forward_fp8")
     return out

@@ -413,6 +413,64 @@ def test_two_graphs_replay_at_once_and_streams():
     assert rs.rs_get_last_device_error() == 0
 
 
+def test_scratch_belongs_to_the_stream_of_the_call():
+    """With an explicit stream, scratch released on return is not handed to work on the current
+    stream while the call still runs."""
+    rs = _rs()
+    M, C, H = 6000, 512, 2048
+    w1, b1, w2, b2 = mlp_weights(C, H, 2)
+    gamma, beta = params(C, BF, 3)
+    x = draw(M, C, BF, 1)
+    want = rs.rs_mlp_forward_fp8(x, w1, b1, w2, b2, gamma, beta)
+    dy = draw(M, C, BF, 2, 0.0)
+    u, stats = rs.rs_ln_forward(x, gamma, beta)
+    wg = rs.rs_ln_backward(dy, x, stats, gamma)
+    n = rs.rs._ws_size("rs_mlp_forward_fp8_ws_bytes", M, C, H)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs, grads = [], []
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)                 # the calls queue up behind this
+    for _ in range(6):
+        outs.append(rs.rs_mlp_forward_fp8(x, w1, b1, w2, b2, gamma, beta, stream=s))
+        grads.append(rs.rs_ln_backward(dy, x, stats, gamma, stream=s))
+        junk = [torch.full((n,), 0x7F, dtype=torch.uint8, device=dev),
+                torch.full((n // 16,), 0x7F, dtype=torch.uint8, device=dev)]
+        del junk
+    torch.cuda.synchronize()
+    for o, g in zip(outs, grads):
+        assert torch.equal(o, want) and all(torch.equal(p, q) for p, q in zip(g, wg))
+
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^32 bytes and 2^31 elements: the last rows against the same rows on
+    their own."""
+    rs = _rs()
+    M, C = (1 << 20) + 77, 2080
+    x = torch.empty(M, C, dtype=BF, device=dev)
+    x[:64].copy_(draw(64, C, BF, 1))
+    x[64:] = x[:64].repeat((M - 64) // 64 + 1, 1)[: M - 64]
+    tail = x[-100:].clone()
+    gamma, beta = params(C, BF, 2)
+    y, stats = rs.rs_ln_forward(x, gamma, beta)
+    want, ws = rs.rs_ln_forward(tail, gamma, beta)
+    assert torch.equal(y[-100:], want) and torch.equal(stats[-100:], ws)
+    dx, _, db = rs.rs_ln_backward(y, x, stats, gamma)
+    assert torch.equal(dx[-100:], rs.rs_ln_backward(want, tail, ws, gamma)[0])
+    del y, dx
+    w = rs.rs_fp8_quantize(draw(136, C, BF, 3, 0.0, 0.05))[0]
+    z = rs.rs_fp8_linear(x, w)
+    assert torch.equal(z[-100:], rs.rs_fp8_linear(tail, w))
+    q, qt, _ = rs.rs_fp8_quantize(x, True, True)
+    p = rs.rs_fp8_quantize(tail)[0]
+    assert torch.equal(q.q[-100:].view(torch.uint8), p.q.view(torch.uint8))
+    last = R.quantized(x[M // 128 * 128:, -8:].double().t().contiguous())
+    at = R.scale_index(C, M)[-8:, -1].to(dev)
+    got = qt.q[-8:, M // 128 * 128:M].double() * torch.exp2(qt.scales[at].double() - 127)[:, None]
+    assert same(got, last)
+    assert rs.rs_get_last_device_error() == 0
+
+
 def test_refusals():
     rs = _rs()
     a, b = operands(4, 24, 64, 1)
