@@ -168,6 +168,7 @@ int rs_ln_quantize(const void* x, int64_t ldx, int M, int C, int dtype, const vo
 
 uint64_t rs_ln_backward_ws_bytes(int M, int C) {
   if (M < 0 || M >= kMaxDim || C < 1 || C > RS_MAX_LN_C) return 0;
+  if (rs::ln_backward_few(M, C)) return 0;
   int sms = 0;
   if (rs::device_sms(&sms) != RS_OK) return 0;
   const uint64_t blocks = M < sms ? (M > 0 ? M : 1) : sms;
@@ -210,10 +211,13 @@ int rs_ln_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, con
   p.C = C;
   p.dx = dx;
   p.lddx = lddx;
-  p.partials = sums ? static_cast<float*>(ws) : nullptr;
+  p.dgamma = dgamma;
+  p.dbeta = dbeta;
+  p.sums = sums;
+  p.partials = static_cast<float*>(ws);
   const bool vec = rows16(dy, lddy, C, es) && rows16(x, ldx, C, es) &&
                    rows16(p.dres, lddres, C, es) && rows16(dx, lddx, C, es) && aligned(gamma, 16);
-  RS_CUDA(rs::launch_ln_backward(p, dtype, vec, sms, dgamma, dbeta, s));
+  RS_CUDA(rs::launch_ln_backward(p, dtype, vec, sms, s));
   return RS_OK;
 }
 

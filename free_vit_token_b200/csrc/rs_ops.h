@@ -56,15 +56,20 @@ struct LnBackward {
   int M, C;
   void* dx;            // or null
   int64_t lddx;
-  float* partials;     // [blocks][2][C], or null: no dgamma, dbeta
+  float* dgamma;       // [C] or null
+  float* dbeta;        // [C] or null
+  bool sums;           // either of them wanted
+  float* partials;     // [blocks][2][C] scratch, unused for a few rows
+  int cluster;         // set by the launcher: blocks of the one cluster, 0 = a grid
 };
 // `vec`: every row of every tensor starts on 16 bytes and is a whole number of 16-byte vectors.
 cudaError_t launch_ln_forward(const LnForward& p, int dtype, bool vec, int num_sms,
                               cudaStream_t s);
 cudaError_t launch_ln_quantize(const LnForward& p, int dtype, int num_sms, cudaStream_t s);
-// Backward, then the sum of the blocks' partials (at most num_sms) into dgamma, dbeta.
-cudaError_t launch_ln_backward(const LnBackward& p, int dtype, bool vec, int num_sms, float* dgamma,
-                               float* dbeta, cudaStream_t s);
+// Backward, then (past a few rows) the sum of the blocks' partials, at most num_sms of them.
+cudaError_t launch_ln_backward(const LnBackward& p, int dtype, bool vec, int num_sms,
+                               cudaStream_t s);
+bool ln_backward_few(int M, int C);  // no scratch for these sizes, whatever the type
 // out[c] = sum_p partials[p][c], p ascending by eights, for n columns: the first `split` of
 // them to out0, the others to out1 (either may be null).
 cudaError_t launch_col_reduce(const float* partials, int P, int n, int split, float* out0,

@@ -159,7 +159,8 @@ def check_bwd(dy, x, gamma, dres, got, eps=EPS):
 @pytest.mark.parametrize("M,C", [(1, 1), (1, 8), (5, 7), (33, 64), (394, 192), (65, 256), (9, 264),
                                  (257, 512), (77, 768), (31, 1001), (300, 1024), (50, 1030),
                                  (17, 2048), (13, 2056), (5, 4096), (7, 4100), (4, 8191), (2, 8192),
-                                 (6000, 40), (4001, 768)])
+                                 (6000, 40), (4001, 768), (512, 192), (513, 192),
+                                 (256, 1000), (300, 2000), (33, 8000)])
 def test_backward(M, C, dtype):
     rs = _rs()
     x, dy, dres = draw(M, C, dtype, 1), draw(M, C, dtype, 2, 0.0), draw(M, C, dtype, 3, 0.0)
@@ -196,7 +197,7 @@ def test_backward_against_differences():
 @pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp32"])
 def test_backward_strided_in_place_and_parts(dtype):
     rs = _rs()
-    M, C, ld = 70, 136, 147
+    M, C, ld = 570, 136, 147
     xs, ys, ds = (draw(M, ld, dtype, k) for k in (1, 2, 3))
     x, dy, dres = xs[:, 3:3 + C], ys[:, 1:1 + C], ds[:, 5:5 + C]
     gamma, _ = params(C, FP, 4)
