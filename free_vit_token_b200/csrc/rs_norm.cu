@@ -20,6 +20,9 @@
 // Rows that do not start on 16 bytes (VEC = false) are copied as the aligned 16-byte units
 // that cover them and shifted into place between shared memory and registers, both ways, so
 // that global memory sees the same wide accesses.
+//
+// Measured (bf16): forward 25104 x 1024 18.8 us (5.4 TB/s), with 8-bit output 23.4 us; gradients
+// 50432 x 768 57 us (5.4 TB/s over x, dy, dres and dx).
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
