@@ -89,12 +89,25 @@ struct Quant {
   uint8_t* scales_t;
   float* partials;     // [quant_chunks(rows, K)][K] column sums, or null
 };
-// Blocks that share out the row tiles of 128 of one column tile: about four per SM in all (two
-// are resident, and a block loads its next tile while it works on one).
+// Blocks that share out the row tiles of 128 of one column tile. 296 blocks are resident (two on
+// each of 148 SMs); of one to four such waves, the number that leaves the longest chain of tiles
+// shortest, a wave's start (its first loads cover nothing) counted as half a tile: 12288 x 4096
+// 608 blocks 46.8 us, 288 blocks 40.5.
 inline int quant_chunks(int rows, int K) {
   const int tiles = (rows + 127) / 128, cols = (K + 127) / 128;
-  const int most = cols < 592 ? (592 + cols - 1) / cols : 1;
-  return tiles < most ? tiles : most;
+  int best = 1;
+  int64_t cost = INT64_MAX;
+  for (int waves = 1; waves <= 4; ++waves) {
+    const int most = 296 * waves / cols;
+    if (most < 1) continue;
+    const int per = (tiles + most - 1) / most, chunks = (tiles + per - 1) / per;
+    const int64_t real = (static_cast<int64_t>(chunks) * cols + 295) / 296;
+    if (real * (2 * per + 1) < cost) {
+      cost = real * (2 * per + 1);
+      best = chunks;
+    }
+  }
+  return best;
 }
 cudaError_t launch_quantize(const Quant& p, int dtype, bool vec, cudaStream_t s, bool pdl = false);
 

