@@ -361,13 +361,13 @@ __global__ void __launch_bounds__(fwd_threads(TPR), TPR <= 256 ? 2 : 1)
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
       cur[i] = live ? read_vec<T, TPR, VEC>(buf, xof, C, l, i) : make_uint4(0, 0, 0, 0);
-    uint64_t s2 = 0;  // pairs of running sums; padding adds zero
+    uint64_t xs[VPL][E / 2];  // the row's values as pairs of fp32
+    uint64_t s2 = 0;          // pairs of running sums; padding adds zero
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      uint64_t f[E / 2];
-      Elem<T>::pairs(cur[i], f);
+      Elem<T>::pairs(cur[i], xs[i]);
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e) s2 = fadd2(s2, f[e]);
+      for (int e = 0; e < E / 2; ++e) s2 = fadd2(s2, xs[i][e]);
     }
     float2 t = f2unpack(s2);
     const float mean = group_sum<TPR>(t.x + t.y, red, group, par) * inv_c;
@@ -375,23 +375,15 @@ __global__ void __launch_bounds__(fwd_threads(TPR), TPR <= 256 ? 2 : 1)
     uint64_t q2 = 0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      uint64_t f[E / 2];
-      Elem<T>::pairs(cur[i], f);
       const int c = col_of<T, TPR>(l, i);
-      if (VEC ? c < C : c + E <= C) {
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) {
-          const uint64_t d = fadd2(f[e], nmean);
-          q2 = ffma2(d, d, q2);
+      for (int e = 0; e < E / 2; ++e) {
+        xs[i][e] = fadd2(xs[i][e], nmean);
+        uint64_t d = xs[i][e];
+        if constexpr (!VEC) {
+          if (c + 2 * e + 1 >= C) d = c + 2 * e >= C ? 0 : static_cast<uint32_t>(d);
         }
-      } else if (!VEC && c < C) {
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) {
-          uint64_t d = fadd2(f[e], nmean);
-          if (c + 2 * e >= C) d = 0;
-          if (c + 2 * e + 1 >= C) d = static_cast<uint32_t>(d);
-          q2 = ffma2(d, d, q2);
-        }
+        if (!VEC || c < C) q2 = ffma2(d, d, q2);
       }
     }
     t = f2unpack(q2);
@@ -402,13 +394,12 @@ __global__ void __launch_bounds__(fwd_threads(TPR), TPR <= 256 ? 2 : 1)
     T* y = static_cast<T*>(p.y) + static_cast<int64_t>(row) * p.ldy;
     const int yof = VEC ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(y) & 15);
     auto affine = [&](int i, float (&f)[E]) {
-      uint64_t f2[E / 2], g[E / 2], b[E / 2];
-      Elem<T>::pairs(cur[i], f2);
+      uint64_t g[E / 2], b[E / 2];
       gamma.get(i, g);
       beta.get(i, b);
 #pragma unroll
       for (int e = 0; e < E / 2; ++e) {
-        const float2 v = f2unpack(ffma2(mul2(fadd2(f2[e], nmean), rstd2), g[e], b[e]));
+        const float2 v = f2unpack(ffma2(mul2(xs[i][e], rstd2), g[e], b[e]));
         f[2 * e] = v.x;
         f[2 * e + 1] = v.y;
       }
@@ -451,6 +442,7 @@ __global__ void __launch_bounds__(fwd_threads(TPR), TPR <= 256 ? 2 : 1)
 #pragma unroll
         for (int i = 0; i < VPL; ++i) a[i] = fmaxf(a[i], __shfl_xor_sync(0xffffffffu, a[i], o));
       uint8_t* q = p.q + static_cast<int64_t>(row) * p.ldq;
+      uint8_t* sc = p.scales + scale_offset(row, 0, p.kq);
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
         const int c = col_of<T, TPR>(l, i);
@@ -463,7 +455,7 @@ __global__ void __launch_bounds__(fwd_threads(TPR), TPR <= 256 ? 2 : 1)
           for (int e = 0; e < 4; ++e) g[e] = f2unpack(mul2(f2pack(f[i][2 * e], f[i][2 * e + 1]), inv2));
           *reinterpret_cast<uint2*>(q + c) = make_uint2(e4m3x4(g[0].x, g[0].y, g[1].x, g[1].y),
                                                         e4m3x4(g[2].x, g[2].y, g[3].x, g[3].y));
-          if ((l & 15) == 0) p.scales[scale_offset(row, c >> 7, p.kq)] = static_cast<uint8_t>(byte);
+          if ((l & 15) == 0) sc[((c >> 9) << 9) + ((c >> 7) & 3)] = static_cast<uint8_t>(byte);
         }
       }
     }
