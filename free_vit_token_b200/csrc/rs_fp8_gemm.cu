@@ -389,11 +389,12 @@ __global__ void __launch_bounds__(kGThreads, 1)
             for (int e = 0; e < 32; ++e)
               if (col0 + 32 * i + e >= p.N) r[i][e] = 0;
         }
-        uint32_t a = 0;
+        float am[2] = {0.f, 0.f};  // two chains; NaN does not enter a maximum
 #pragma unroll
         for (int i = 0; i < kCols / 32; ++i)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) a = max(a, r[i][e] & 0x7FFFFFFFu);
+          for (int e = 0; e < 32; ++e) am[e & 1] = fmaxf(am[e & 1], fabsf(__uint_as_float(r[i][e])));
+        uint32_t a = __float_as_uint(fmaxf(am[0], am[1]));
         if (a >= kInfBits) {
           a = 0;
 #pragma unroll
