@@ -23,7 +23,9 @@ __device__ __forceinline__ uint64_t gelu2_logit(uint64_t z2) {
   q = ffma2(q, t, pair_of(-RS_GELU_LOGIT_Q1));
   q = ffma2(q, t, pair_of(-RS_GELU_LOGIT_Q0));
   const float2 x = f2unpack(mul2(q, z2));
-  // up to 2^60, so that the product of two stays finite (the CDF is below 1e-17 there)
+  // up to 2^60, so that the product of two stays finite: past it GELU is z 2^-60 where it should
+  // vanish (below 1e-12 for z > -1e6; -inf stays -inf). A degree-4 fit without the bound on t and
+  // with this one on z instead takes one more FMA and measured 6% slower.
   const float2 d = f2unpack(
       fadd2(f2pack(ex2_approx(fminf(x.x, 60.f)), ex2_approx(fminf(x.y, 60.f))), pair_of(1.f)));
   float r;
