@@ -163,10 +163,12 @@ __global__ void __launch_bounds__(kGThreads, 1)
       const int a_row = m_blk * kTileM + static_cast<int>(rank) * kGM;
       const int n0 = n_blk * BN;
       const int b_row = n0 + static_cast<int>(rank) * kBRows;
+      // test hook: leave one stage unfilled so the consumer's wait runs out
+      const int skip_kb = (blockIdx.x == 0 && tile == unit0) ? p.debug_skip_kb : -1;
       bool ok = true;
       for (int kb = 0; kb < KB; ++kb) {
         if (!warp_wait(&empty[stage], phase ^ 1u, wc)) { ok = false; break; }
-        if (elect_one()) {
+        if (kb != skip_kb && elect_one()) {
           const bool scales = (kb & 3) == 0;
           if (leader) mbar_arrive_expect_tx(&full[stage], scales ? kTx + kTxScales : kTx);
           uint8_t* dA = sA + stage * kGABytes;
@@ -192,9 +194,11 @@ __global__ void __launch_bounds__(kGThreads, 1)
           }
         }
         __syncwarp();
-        const uint32_t bit = 1u << stage;
-        pend_mask |= bit;
-        pend_phase = (pend_phase & ~bit) | (phase << stage);
+        if (kb != skip_kb) {
+          const uint32_t bit = 1u << stage;
+          pend_mask |= bit;
+          pend_phase = (pend_phase & ~bit) | (phase << stage);
+        }
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
       if (!ok) break;

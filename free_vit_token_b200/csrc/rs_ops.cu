@@ -82,10 +82,12 @@ rs::LnForward norm_args(const void* x, int64_t ldx, int M, int C, const void* ga
   return p;
 }
 
-int gemm(rs::Fp8Gemm p, int out_dtype, cudaStream_t s, bool pdl) {
+int gemm(rs::Fp8Gemm p, int out_dtype, cudaStream_t s, bool pdl, int debug_skip_kb = -1,
+         unsigned long long timeout_ns = rs::kDefaultTimeoutNs) {
   int sms = 0;
   RS_TRY(rs::device_flag(&sms, &p.err));
-  p.timeout_ns = rs::kDefaultTimeoutNs;
+  p.timeout_ns = timeout_ns;
+  p.debug_skip_kb = debug_skip_kb;
   const int es = out_dtype == RS_E4M3 ? 1 : elem_bytes(out_dtype);
   p.direct = !(aligned(p.out, 16) && p.ldo * es % 16 == 0);
   p.rvec = p.resid != nullptr && aligned(p.resid, 16) && p.ldr * es % 16 == 0;
@@ -268,10 +270,11 @@ int rs_fp8_quantize(const void* x, int64_t ldx, int rows, int K, int dtype, void
   return RS_OK;
 }
 
-int rs_fp8_gemm(const void* a, int64_t lda, const void* scales_a, const void* b, int64_t ldb,
-                const void* scales_b, int M, int N, int K, const void* bias, int gelu,
-                const void* resid, int64_t ldr, void* out, int64_t ldo, int out_dtype,
-                void* out_scales, void* stream) {
+static int fp8_gemm(const void* a, int64_t lda, const void* scales_a, const void* b, int64_t ldb,
+                    const void* scales_b, int M, int N, int K, const void* bias, int gelu,
+                    const void* resid, int64_t ldr, void* out, int64_t ldo, int out_dtype,
+                    void* out_scales, cudaStream_t s, int debug_skip_kb,
+                    unsigned long long timeout_ns) {
   RS_TRY(check_gemm_dims(M, N, K));
   if (out_dtype != RS_BF16 && out_dtype != RS_FP32 && out_dtype != RS_E4M3) return RS_ERR_SHAPE;
   const int es = out_dtype == RS_E4M3 ? 1 : elem_bytes(out_dtype);
@@ -304,7 +307,27 @@ int rs_fp8_gemm(const void* a, int64_t lda, const void* scales_a, const void* b,
   p.out = out;
   p.ldo = ldo;
   p.out_scales = static_cast<uint8_t*>(out_scales);
-  return gemm(p, out_dtype, static_cast<cudaStream_t>(stream), false);
+  return gemm(p, out_dtype, s, false, debug_skip_kb, timeout_ns);
+}
+
+int rs_fp8_gemm(const void* a, int64_t lda, const void* scales_a, const void* b, int64_t ldb,
+                const void* scales_b, int M, int N, int K, const void* bias, int gelu,
+                const void* resid, int64_t ldr, void* out, int64_t ldo, int out_dtype,
+                void* out_scales, void* stream) {
+  return fp8_gemm(a, lda, scales_a, b, ldb, scales_b, M, N, K, bias, gelu, resid, ldr, out, ldo,
+                  out_dtype, out_scales, static_cast<cudaStream_t>(stream), -1, rs::kDefaultTimeoutNs);
+}
+
+int rs_debug_fp8_skip_load(const void* a, int64_t lda, const void* scales_a, const void* b,
+                           int64_t ldb, const void* scales_b, int M, int N, int K, void* out,
+                           int64_t ldo, int out_dtype, void* out_scales, int skip_kblock,
+                           int timeout_us, void* stream) {
+  if (K < 1 || skip_kblock < 0 || skip_kblock >= (K - 1) / 128 + 1 || timeout_us < 1 ||
+      timeout_us > 10000000)
+    return RS_ERR_SHAPE;
+  return fp8_gemm(a, lda, scales_a, b, ldb, scales_b, M, N, K, nullptr, 0, nullptr, 0, out, ldo,
+                  out_dtype, out_scales, static_cast<cudaStream_t>(stream), skip_kblock,
+                  static_cast<unsigned long long>(timeout_us) * 1000ull);
 }
 
 uint64_t rs_fp8_linear_ws_bytes(int M, int K) {

@@ -135,6 +135,7 @@ struct Fp8Gemm {
   int kqo;               // kOutQ8: scale tiles along N
   int* err;
   unsigned long long timeout_ns;
+  int debug_skip_kb;     // test hook: CTA 0 skips this K block's loads of its first tile (-1: off)
   int n_blocks, num_tiles;  // set by the launcher
 };
 // RS_OK or an error status.

@@ -72,6 +72,8 @@ SIGNATURES = {
     "rs_fp8_quantize_ws_bytes": (_u, [_i, _i]),
     "rs_fp8_gemm": (_i, [_vp, _l, _vp, _vp, _l, _vp, _i, _i, _i, _vp, _i, _vp, _l, _vp, _l, _i, _vp,
                          _vp]),
+    "rs_debug_fp8_skip_load": (_i, [_vp, _l, _vp, _vp, _l, _vp, _i, _i, _i, _vp, _l, _i, _vp, _i, _i,
+                                    _vp]),
     "rs_fp8_linear": (_i, [_vp, _l, _i, _i, _i, _vp, _l, _vp, _vp, _i, _vp, _l, _vp, _l, _vp, _u,
                            _vp]),
     "rs_fp8_linear_ws_bytes": (_u, [_i, _i]),
@@ -885,3 +887,21 @@ def rs_mlp_forward_fp8(x: torch.Tensor, w1: Fp8, b1, w2: Fp8, b2, gamma, beta,
                                   _rows(out, "out", dev, bf, C, M)[0], pws, nws, _stream(None))
     _check(st, "rs_mlp_forward_fp8")
     return out
+
+
+def rs_debug_fp8_skip_load(a: Fp8, b: Fp8, out, skip_kblock: int, timeout_us: int,
+                           stream=None) -> None:
+    """Test hook: rs_fp8_gemm with one K block's load withheld (see include/rs.h)."""
+    M, N, K = a.rows, b.rows, a.K
+    dev = _device(a.q, "a")
+    pa, lda, sa = _fp8(a, "a", dev)
+    pb, ldb, sb = _fp8(b, "b", dev, K=K)
+    if isinstance(out, Fp8):
+        po, ldo, so = _fp8(out, "out", dev, M, N)
+        dt = RS_E4M3
+    else:
+        po, ldo, _ = _rows(out, "out", dev, None, N, M)
+        so, dt = None, _float_type(out)
+    _check(lib().rs_debug_fp8_skip_load(pa, lda, sa, pb, ldb, sb, M, N, K, po, ldo, dt, so,
+                                        int(skip_kblock), int(timeout_us), _stream(stream)),
+           "rs_debug_fp8_skip_load")

@@ -462,6 +462,17 @@ int rs_fp8_gemm(const void* a, int64_t lda, const void* scales_a, const void* b,
                 const void* resid, int64_t ldr, void* out, int64_t ldo, int out_dtype,
                 void* out_scales, void* stream);
 
+/* Test hook of rs_fp8_gemm's failure path: rs_fp8_gemm (without bias, activation or residual) in
+ * which CTA 0's producer leaves K block `skip_kblock` (blocks of 128, 0 <= skip_kblock <
+ * ceil(K / 128)) of its first tile unloaded, every pipeline wait limited to timeout_us
+ * microseconds (1 .. 10^7). The wait for it runs out: the kernel records RS_ERR_DEVICE_TIMEOUT in
+ * the device flag, drains its own copies and MMAs, frees its tensor memory and returns. `out` is
+ * left partly unwritten. */
+int rs_debug_fp8_skip_load(const void* a, int64_t lda, const void* scales_a, const void* b,
+                           int64_t ldb, const void* scales_b, int M, int N, int K, void* out,
+                           int64_t ldo, int out_dtype, void* out_scales, int skip_kblock,
+                           int timeout_us, void* stream);
+
 /* A linear layer with its weight held in 8 bits: x [M, K] bf16 is quantised along K, then
  * out [M, N] bf16 = act(x W^T + bias) + resid as rs_fp8_gemm. wq [N, ldw], scales_w: W [N, K]
  * in 8-bit blocks. A few rows (up to 16, or 32 for N <= 8192, with K <= 8192) run as one launch,

@@ -471,6 +471,26 @@ def test_offsets_past_32_bits():
     assert rs.rs_get_last_device_error() == 0
 
 
+@pytest.mark.parametrize("M,N,K,skip", [(100, 128, 1024, 3), (300, 20000, 512, 0), (2000, 2048, 2048, 9)],
+                         ids=["128x128", "single", "pair"])
+@pytest.mark.parametrize("dtype", [BF, E4], ids=["bf16", "e4m3"])
+def test_a_withheld_load_times_out_and_the_next_call_is_right(M, N, K, skip, dtype):
+    rs = _rs()
+    a, b = operands(M, N, K, 3)
+    want = rs.rs_fp8_gemm(a, b, out_dtype=dtype)
+    out = rs.rs.Fp8(want.q.clone(), want.scales.clone(), M, N) if dtype == E4 else want.clone()
+    assert rs.rs_get_last_device_error() == 0
+    rs.rs_debug_fp8_skip_load(a, b, out, skip, 2000)
+    assert rs.rs_get_last_device_error() == rs.rs.RS_ERR_DEVICE_TIMEOUT
+    assert rs.rs_get_last_device_error() == 0
+    got = rs.rs_fp8_gemm(a, b, out_dtype=dtype)
+    if dtype == E4:
+        assert torch.equal(R.stored(got), R.stored(want))
+    else:
+        assert torch.equal(got, want)
+    assert rs.rs_get_last_device_error() == 0
+
+
 def test_refusals():
     rs = _rs()
     a, b = operands(4, 24, 64, 1)

@@ -86,6 +86,13 @@ def test_gemm(kw, want):
     assert gemm(**kw) == want
 
 
+@pytest.mark.parametrize("skip,us,want", [(-1, 100, SHAPE), (2, 100, SHAPE), (0, 0, SHAPE),
+                                          (0, 10000001, SHAPE), (1, 100, NULL)])
+def test_debug_skip_load(skip, us, want):
+    assert rs.lib().rs_debug_fp8_skip_load(None, 208, F, F, 208, F, 4, 24, 200, F, 24, BF, None, skip, us,
+                                           None) == want
+
+
 def linear(x=F, ldx=200, M=40, K=200, N=24, w=F, ldw=208, sw=F, bias=F, gelu=0, r=None, ldr=24, o=F,
            ldo=24, ws=F, n=BIG):
     return rs.lib().rs_fp8_linear(x, ldx, M, K, N, w, ldw, sw, bias, gelu, r, ldr, o, ldo, ws, n, None)
