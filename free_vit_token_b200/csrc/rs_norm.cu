@@ -21,7 +21,7 @@
 // that cover them and shifted into place between shared memory and registers, both ways, so
 // that global memory sees the same wide accesses.
 //
-// Measured (bf16): forward 25104 x 1024 18.8 us (5.4 TB/s), with 8-bit output 23.4 us; gradients
+// Measured (bf16): forward 25104 x 1024 18.5 us (5.6 TB/s), with 8-bit output 23.0 us; gradients
 // 50432 x 768 57 us (5.4 TB/s over x, dy, dres and dx).
 #include <cstdint>
 #include <cuda_bf16.h>

@@ -262,11 +262,13 @@ int rs_fp8_quantize(const void* x, int64_t ldx, int rows, int K, int dtype, void
   p.qt = static_cast<uint8_t*>(qt);
   p.ldqt = ldqt;
   p.scales_t = static_cast<uint8_t*>(scales_t);
-  p.partials = colsum ? static_cast<float*>(ws) : nullptr;
+  const bool direct = colsum && rs::quant_direct(rows);
+  p.partials = direct ? colsum : colsum ? static_cast<float*>(ws) : nullptr;
+  p.chunks = direct ? 1 : rs::quant_chunks(rows, K);
   const bool vec = aligned(x, 16) && ldx * es % 16 == 0 && K % 8 == 0;
   RS_CUDA(rs::launch_quantize(p, dtype, vec, s));
-  if (colsum)
-    RS_CUDA(rs::launch_col_reduce(p.partials, rs::quant_chunks(rows, K), K, K, colsum, nullptr, s, true));
+  if (colsum && !direct)
+    RS_CUDA(rs::launch_col_reduce(p.partials, p.chunks, K, K, colsum, nullptr, s, true));
   return RS_OK;
 }
 
@@ -378,6 +380,7 @@ int rs_fp8_linear(const void* x, int64_t ldx, int M, int K, int N, const void* w
   qp.q = static_cast<uint8_t*>(ws);
   qp.ldq = static_cast<int64_t>(w.ld);
   qp.scales = qp.q + w.scales;
+  qp.chunks = rs::quant_chunks(M, K);
   rs::Fp8Gemm p{};
   p.a = qp.q;
   p.lda = qp.ldq;
@@ -444,7 +447,9 @@ int rs_fp8_linear_backward(const void* dy, int64_t lddy, int M, int N, int K, co
     qp.ldqt = static_cast<int64_t>(wtr.ld);
     qp.scales_t = qp.qt + wtr.scales;
   }
-  if (db) qp.partials = reinterpret_cast<float*>(base + w.bytes + wtr.bytes);
+  const bool direct = db && rs::quant_direct(M);
+  if (db) qp.partials = direct ? db : reinterpret_cast<float*>(base + w.bytes + wtr.bytes);
+  qp.chunks = direct ? 1 : rs::quant_chunks(M, N);
   RS_CUDA(rs::launch_quantize(qp, RS_BF16, aligned(dy, 16) && lddy % 8 == 0 && N % 8 == 0, s));
   if (dx) {
     rs::Fp8Gemm p{};
@@ -476,8 +481,8 @@ int rs_fp8_linear_backward(const void* dy, int64_t lddy, int M, int N, int K, co
     p.ldo = lddw;
     RS_TRY(gemm(p, dw_dtype, s, true));
   }
-  if (db)
-    RS_CUDA(rs::launch_col_reduce(qp.partials, rs::quant_chunks(M, N), N, N, db, nullptr, s, true));
+  if (db && !direct)
+    RS_CUDA(rs::launch_col_reduce(qp.partials, qp.chunks, N, N, db, nullptr, s, true));
   return RS_OK;
 }
 

@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2) quantize_kernel(c
 template <typename T, bool VEC>
 static cudaError_t pick(const Quant& p, cudaStream_t s, bool pdl) {
   const dim3 block(256);
-  const dim3 grid((p.K + kQTile - 1) / kQTile, quant_chunks(p.rows, p.K));
+  const dim3 grid((p.K + kQTile - 1) / kQTile, p.chunks);
   if (p.qt == nullptr) return launch(quantize_kernel<T, VEC, true, false>, grid, block, 0, s, pdl, p);
   if (p.q == nullptr) return launch(quantize_kernel<T, VEC, false, true>, grid, block, 0, s, pdl, p);
   return launch(quantize_kernel<T, VEC, true, true>, grid, block, 0, s, pdl, p);

@@ -635,6 +635,12 @@ def _fp8_empty(rows: int, K: int, device) -> Fp8:
                torch.empty(_scale_bytes(rows, K), dtype=torch.uint8, device=device), rows, K)
 
 
+def _fp8_new(rows: int, K: int, device):
+    """A new Fp8 with its (q address, row stride, scales address)."""
+    t = _fp8_empty(rows, K, device)
+    return t, t.q.data_ptr() or None, (K + 15) // 16 * 16, t.scales.data_ptr() or None
+
+
 def _fp8(t: Fp8, name: str, dev: int, rows: Optional[int] = None, K: Optional[int] = None):
     """(q address, row stride, scales address) of a quantised operand."""
     q, s, r, k = t
@@ -689,8 +695,9 @@ def rs_ln_quantize(x: torch.Tensor, gamma: Optional[torch.Tensor] = None,
     C = x.shape[-1]
     pdt, pg, pb = _params(x, dev, C, gamma, beta)
     if out is None:
-        out = _fp8_empty(M, C, x.device)
-    q, ldq, sc = _fp8(out, "out", dev, M, C)
+        out, q, ldq, sc = _fp8_new(M, C, x.device)
+    else:
+        q, ldq, sc = _fp8(out, "out", dev, M, C)
     _check(lib().rs_ln_quantize(px, ldx, M, C, dt, pg, pb, pdt, eps, q, ldq, sc,
                                 _vec(stats, "stats", dev, 2 * M, torch.float32), _stream(None)),
            "rs_ln_quantize")
@@ -719,12 +726,17 @@ def rs_ln_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor,
         pdx, lddx, _ = _rows(dx, "dx", dev, x.dtype, C, M)
     if dgamma is None:
         dgamma = torch.empty(C, dtype=f32, device=device)
+        pdg = dgamma.data_ptr() or None
+    else:
+        pdg = _vec(dgamma, "dgamma", dev, C, f32)
     if dbeta is None:
         dbeta = torch.empty(C, dtype=f32, device=device)
+        pdb = dbeta.data_ptr() or None
+    else:
+        pdb = _vec(dbeta, "dbeta", dev, C, f32)
     pw, nw, ws = _ws(ws, device, dev, "rs_ln_backward_ws_bytes", M, C)
     st = lib().rs_ln_backward(pdy, lddy, px, ldx, pdr, lddr, _vec(stats, "stats", dev, 2 * M, f32),
-                              pg, pdt, M, C, dt, pdx, lddx, _vec(dgamma, "dgamma", dev, C, f32),
-                              _vec(dbeta, "dbeta", dev, C, f32), pw, nw, _stream(None))
+                              pg, pdt, M, C, dt, pdx, lddx, pdg, pdb, pw, nw, _stream(None))
     _check(st, "rs_ln_backward")
     return dx, dgamma, dbeta
 
@@ -750,12 +762,14 @@ def rs_fp8_quantize(x: torch.Tensor, rows: bool = True, cols: bool = False, cols
     ldq = ldqt = nw = 0
     if rows:
         if out is None:
-            out = _fp8_empty(M, K, device)
-        q, ldq, sc = _fp8(out, "out", dev, M, K)
+            out, q, ldq, sc = _fp8_new(M, K, device)
+        else:
+            q, ldq, sc = _fp8(out, "out", dev, M, K)
     if cols:
         if out_t is None:
-            out_t = _fp8_empty(K, M, device)
-        qt, ldqt, sct = _fp8(out_t, "out_t", dev, K, M)
+            out_t, qt, ldqt, sct = _fp8_new(K, M, device)
+        else:
+            qt, ldqt, sct = _fp8(out_t, "out_t", dev, K, M)
     if colsum:
         sums = torch.empty(K, dtype=torch.float32, device=device)
         ps = sums.data_ptr()
@@ -782,15 +796,18 @@ def rs_fp8_gemm(a: Fp8, b: Fp8, bias: Optional[torch.Tensor] = None, gelu: bool 
     so, pr, ldr = None, None, N
     if out_dtype is torch.float8_e4m3fn:
         if out is None:
-            out = _fp8_empty(M, N, device)
-        po, ldo, so = _fp8(out, "out", dev, M, N)
+            out, po, ldo, so = _fp8_new(M, N, device)
+        else:
+            po, ldo, so = _fp8(out, "out", dev, M, N)
         dt = RS_E4M3
     else:
         if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
             raise ValueError("out_dtype: bfloat16, float32 or float8_e4m3fn")
         if out is None:
             out = torch.empty(M, N, dtype=out_dtype, device=device)
-        po, ldo, _ = _rows(out, "out", dev, out_dtype, N, M)
+            po, ldo = out.data_ptr() or None, N
+        else:
+            po, ldo, _ = _rows(out, "out", dev, out_dtype, N, M)
         dt = _DTYPES[out_dtype]
     if resid is not None:
         pr, ldr, _ = _rows(resid, "resid", dev, out_dtype, N, M)
@@ -878,13 +895,15 @@ def rs_mlp_forward_fp8(x: torch.Tensor, w1: Fp8, b1, w2: Fp8, b2, gamma, beta,
     p2, ld2, s2 = _fp8(w2, "w2", dev, C, H)
     if out is None:
         out = torch.empty_like(x)
+        po = out.data_ptr() or None
     elif not out.is_contiguous():
         raise ValueError("out must be contiguous")
+    else:
+        po = _rows(out, "out", dev, bf, C, M)[0]
     pws, nws, ws = _ws(ws, x.device, dev, "rs_mlp_forward_fp8_ws_bytes", M, C, H)
     st = lib().rs_mlp_forward_fp8(px, M, C, H, p1, ld1, s1, _vec(b1, "b1", dev, H, bf), p2, ld2, s2,
                                   _vec(b2, "b2", dev, C, bf), _vec(gamma, "gamma", dev, C, bf),
-                                  _vec(beta, "beta", dev, C, bf),
-                                  _rows(out, "out", dev, bf, C, M)[0], pws, nws, _stream(None))
+                                  _vec(beta, "beta", dev, C, bf), po, pws, nws, _stream(None))
     _check(st, "rs_mlp_forward_fp8")
     return out
 
