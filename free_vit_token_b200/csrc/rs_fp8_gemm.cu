@@ -21,7 +21,7 @@
 //
 // Measured, back to back: 8192^3 420 us (2.6 PFLOP/s; 300 us with the operand loads left out, and
 // 511 us sustained, where the power cap holds the clock near 1.06 GHz), 25104 x 4096 -> 1024
-// 88 us, 25104 x 1024 -> 4096 103 us, with GELU and 8-bit output 109 us.
+// 88 us, 25104 x 1024 -> 4096 103 us, with GELU and 8-bit output 106 us.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

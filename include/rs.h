@@ -392,7 +392,8 @@ int rs_debug_fc1_skip_load(const void* x, int M, int C, int H, const void* W1, c
  *   - There is no library workspace: calls that need scratch take `ws` (256-byte aligned) and
  *     `ws_bytes`, at least what the matching _ws_bytes function says (0 where a call needs
  *     none, ws may then be NULL, or the sizes are invalid). Scratch holds nothing between calls, so calls with their own scratch may
- *     overlap on any streams and be captured into any graphs.
+ *     overlap on any streams and be captured into any graphs (the products once the device's
+ *     status flag exists, as above).
  *   - 0 <= rows < 2^27; other sizes as stated. Without rows nothing is launched except what
  *     sets gradient sums to zero.
  *   - Outputs may not overlap inputs except where stated.
