@@ -177,6 +177,37 @@ def test_gemm_scales_reach_their_rows_and_blocks():
     assert ((got.double() - want).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("ea,eb", [(-126, 100), (-122, 118), (118, -120), (0, -126)])
+def test_gemm_scales_at_the_ends_of_their_range(ea, eb):
+    """Scale bytes down to 0 (2^-127) and up to 2^112 in one operand."""
+    rs = _rs()
+    for M in (5, 300):
+        x = draw(M, 300, FP, 2) * 2.0 ** ea
+        w = draw(200, 300, FP, 3) * 2.0 ** eb
+        a, b = rs.rs_fp8_quantize(x)[0], rs.rs_fp8_quantize(w)[0]
+        assert same(R.stored(a), R.quantized(x.double()))
+        got = rs.rs_fp8_gemm(a, b, out_dtype=FP)
+        want, tol = epilogue_tol(a, b, None, False, None, FP)
+        # results below fp32's normal range may be flushed to zero
+        assert ((got.double() - want).abs() <= tol + 2.0 ** -126).all()
+
+
+def test_norm_with_infinite_gamma():
+    rs = _rs()
+    x = draw(9, 256, BF, 1)
+    gamma, beta = params(256, BF, 2)
+    gamma[7] = float("inf")
+    v = R.stored(rs.rs_ln_quantize(x, gamma, beta))
+    assert v[:, 7].isnan().all() and not v[:, :7].isnan().any() and not v[:, 8:].isnan().any()
+    g2 = gamma.clone()
+    g2[7] = 0
+    b2 = beta.clone()
+    b2[7] = 0
+    w = R.stored(rs.rs_ln_quantize(x, g2, b2))
+    keep = [c for c in range(256) if c != 7]
+    assert torch.equal(v[:, keep], w[:, keep])        # the block's scale is its finite values'
+
+
 def test_gemm_nan_and_infinity_stay_in_their_row():
     rs = _rs()
     x, w = draw(200, 300, BF, 1), draw(150, 300, BF, 2)
