@@ -13,7 +13,7 @@ namespace rs {
 int device_sms(int* num_sms);
 int device_flag(int* num_sms, int** err);
 // Allows `kern` `bytes` of dynamic shared memory on the current device, once per device (`done`
-// is the kernel's own, one bit per device): the call costs as much as a third of a launch.
+// is the kernel's own, one bit per device) instead of once per launch.
 template <typename... A>
 inline cudaError_t allow_smem(void (*kern)(A...), int bytes, std::atomic<uint64_t>& done) {
   int dev = 0;
