@@ -671,7 +671,7 @@ int go(Fp8Gemm p, int num_sms, cudaStream_t s, bool pdl) {
 // and each epilogue is short. Else 256 columns, by single CTAs while the reduction is short (a
 // pair's accumulator goes back and forth between two SMs once a tile) and by CTA pairs on 256
 // rows past that (a third less operand traffic). Measured 16384 x 4096, single / pair, us: plain
-// K = 512 42 / 49, K = 768 61 / 55; GELU K = 768 64 / 67, K = 1536 104 / 98.
+// K = 512 42 / 49, K = 768 61 / 55; GELU K = 768 68 / 74, K = 1024 77 / 80, K = 1536 102 / 97.
 template <int OUT>
 int pick(const Fp8Gemm& p, int num_sms, cudaStream_t s, bool pdl) {
   const int64_t small = (static_cast<int64_t>(p.M) + 127) / 128 * ((static_cast<int64_t>(p.N) + 127) / 128);

@@ -10,27 +10,33 @@ namespace rs {
 
 __device__ __forceinline__ uint64_t pair_of(float c) { return f2pack(c, c); }
 
-// GELU of two fp32 lanes through a logistic form of the normal CDF (rs_gelu_logit.h, max
-// |error| 1.5e-5 with the approximate 2^x and reciprocal). Against the polynomials of
-// rs_gelu.cuh it takes half the FMAs, three instructions of the exponential unit a pair (one
-// reciprocal serves both lanes: 1/a = b / (ab)) and no choice by range: 50432 x 384 -> 1536 on
-// values past the short polynomial's range 92 -> 73 us a call.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// GELU of two fp32 lanes through a logistic form of the normal CDF (rs_gelu_logit.h): within
+// 2^-18 of its value for z >= -4.4 and within 3e-8 below, with the approximate 2^x and reciprocal.
+// Nothing bounds the exponent: 2^x overflows where GELU vanishes, and infinities and NaN go where
+// z Phi(z) sends them. So each lane takes a reciprocal of its own: one for both (1/(ab)) needs a
+// bound, which leaves far negative z at a multiple of z. Against a degree of 3 and one reciprocal,
+// 1.4e-5 off, 50432 x 384 -> 1536 takes 68 us for 62, 25104 x 1024 -> 4096 to blocks 121 for 111.
 __device__ __forceinline__ uint64_t gelu2_logit(uint64_t z2) {
-  const float2 s = f2unpack(mul2(z2, z2));
-  const uint64_t t = f2pack(fminf(s.x, RS_GELU_LOGIT_T), fminf(s.y, RS_GELU_LOGIT_T));
-  uint64_t q = pair_of(-RS_GELU_LOGIT_Q3);
+  const uint64_t t = mul2(z2, z2);
+  uint64_t q = pair_of(-RS_GELU_LOGIT_Q9);
+  q = ffma2(q, t, pair_of(-RS_GELU_LOGIT_Q8));
+  q = ffma2(q, t, pair_of(-RS_GELU_LOGIT_Q7));
+  q = ffma2(q, t, pair_of(-RS_GELU_LOGIT_Q6));
+  q = ffma2(q, t, pair_of(-RS_GELU_LOGIT_Q5));
+  q = ffma2(q, t, pair_of(-RS_GELU_LOGIT_Q4));
+  q = ffma2(q, t, pair_of(-RS_GELU_LOGIT_Q3));
   q = ffma2(q, t, pair_of(-RS_GELU_LOGIT_Q2));
   q = ffma2(q, t, pair_of(-RS_GELU_LOGIT_Q1));
   q = ffma2(q, t, pair_of(-RS_GELU_LOGIT_Q0));
   const float2 x = f2unpack(mul2(q, z2));
-  // up to 2^60, so that the product of two stays finite: past it GELU is z 2^-60 where it should
-  // vanish (below 1e-12 for z > -1e6; -inf stays -inf). A degree-4 fit without the bound on t and
-  // with this one on z instead takes one more FMA and measured 6% slower.
-  const float2 d = f2unpack(
-      fadd2(f2pack(ex2_approx(fminf(x.x, 60.f)), ex2_approx(fminf(x.y, 60.f))), pair_of(1.f)));
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d.x * d.y));
-  return mul2(z2, f2pack(r * d.y, r * d.x));
+  const float2 d = f2unpack(fadd2(f2pack(ex2_approx(x.x), ex2_approx(x.y)), pair_of(1.f)));
+  return mul2(z2, f2pack(rcp_approx(d.x), rcp_approx(d.y)));
 }
 
 }  // namespace rs

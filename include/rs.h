@@ -452,7 +452,8 @@ uint64_t rs_fp8_quantize_ws_bytes(int rows, int K);
 
 /* out [M, N] = act(A B^T + bias) + resid for A [M, K] and B [N, K] in 8-bit blocks along K:
  * products of the stored values, accumulated in fp32 (in the tensor cores).
- *   bias [N] bf16 or NULL (16-byte aligned); gelu: 1 for the exact GELU, 0 for none
+ *   bias [N] bf16 or NULL (16-byte aligned); gelu: 0 for none, 1 for GELU, z Phi(z) (not its tanh
+ *   form), within 2^-18 of its value for z >= -4.4 and within 3e-8 below, before out's rounding
  *   resid [M, N] of out's type or NULL (added after act; may be out; not with RS_E4M3)
  *   out: `out_dtype` RS_BF16, RS_FP32, or RS_E4M3, which stores 8-bit blocks along N (ldo a
  *   multiple of 16, scales to out_scales, else NULL; bytes from a row's end to the next
