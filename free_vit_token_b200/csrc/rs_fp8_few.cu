@@ -183,7 +183,16 @@ __global__ void __launch_bounds__(kFThreads)
 #pragma unroll
     for (int t = 0; t < T; ++t)
       sD[t * 128 + warp * 32 + lane] = nb > 0 ? __uint_as_float(r[t]) : 0.f;
+    // Tensor memory goes back before this CTA waits for its cluster. A CTA pair of another stream
+    // may hold all of it on one SM and wait for these columns on another (the bf16 product's
+    // 64-column tiles leave room beside them), while this CTA's partner waits for it there:
+    // what is held may not wait.
     tc_fence_before_sync();
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (warp == 0) {
+      tc_fence_after_sync();
+      tmem_dealloc(tmem, kFTmemCols);
+    }
   }
   if (p.split > 1)
     cluster_sync();
@@ -208,14 +217,7 @@ __global__ void __launch_bounds__(kFThreads)
       p.out[static_cast<int64_t>(t) * p.ldo + n] = __float2bfloat16_rn(v);
     }
   }
-  if (p.split > 1)
-    cluster_sync();  // the others have read this CTA's sums
-  else
-    __syncthreads();
-  if (warp == 0) {
-    tc_fence_after_sync();
-    tmem_dealloc(tmem, kFTmemCols);
-  }
+  if (p.split > 1) cluster_sync();  // the others have read this CTA's sums
 }
 
 template <int T>
