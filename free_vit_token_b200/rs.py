@@ -504,6 +504,7 @@ def rs_debug_attn_skip_load(qkv: torch.Tensor, heads: int, out: torch.Tensor, sk
 # ------------------------------------------------------------------ layer norm, 8-bit blocks
 RS_BF16, RS_FP16, RS_FP32, RS_E4M3 = 0, 1, 2, 3
 RS_MAX_LN_C = 8192
+_INT_MAX = 2 ** 31 - 1
 _DTYPES = {torch.bfloat16: RS_BF16, torch.float16: RS_FP16, torch.float32: RS_FP32}
 
 
@@ -550,6 +551,8 @@ def _rows(t: torch.Tensor, name: str, dev: int, dtype: Optional[torch.dtype] = N
         if n > 1 and ld < w:
             raise ValueError(f"{name}: rows overlap")
         ld = max(ld, w)
+    if n > _INT_MAX or w > _INT_MAX:  # ctypes would pass on what 32 bits hold of them
+        raise ValueError(f"{name}: sizes below 2^31 wanted, got [{n}, {w}]")
     if width is not None and w != width:
         raise ValueError(f"{name}: rows of {width} wanted, got {w}")
     if rows is not None and n != rows:
@@ -647,7 +650,7 @@ def _fp8(t: Fp8, name: str, dev: int, rows: Optional[int] = None, K: Optional[in
     if (rows is not None and r != rows) or (K is not None and k != K):
         raise ValueError(f"{name}: [{rows}, {K}] wanted, got [{r}, {k}]")
     pq, ld, _ = _rows(q, name, dev, torch.float8_e4m3fn, rows=r)
-    if q.shape[-1] < k:
+    if not 0 <= k <= q.shape[-1]:
         raise ValueError(f"{name}: rows shorter than K")
     n = s.numel()
     if n < _scale_bytes(r, k):
@@ -742,6 +745,9 @@ def rs_ln_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor,
 
 
 def rs_fp8_scale_bytes(rows: int, K: int) -> int:
+    """Bytes of the scales of a [rows, K] matrix; 0 for sizes that the library does not take."""
+    if not (0 <= rows <= _INT_MAX and 0 <= K <= _INT_MAX):
+        return 0
     return int(lib().rs_fp8_scale_bytes(int(rows), int(K)))
 
 

@@ -1,0 +1,35 @@
+"""The Python binding of the layer norm and 8-bit calls: what it passes on and keeps (no GPU)."""
+import pytest
+import torch
+
+import free_vit_token_b200.rs as rs
+
+BF = torch.bfloat16
+
+
+@pytest.mark.parametrize("shape", [((1 << 32) + 4, 0), (1 << 31, 8), (1 << 16, 1 << 16, 1),
+                                   (0, (1 << 32) + 64), (0, 1 << 31), (1, (1 << 32) + 64)])
+def test_sizes_past_an_int_are_refused(shape):
+    """They would reach the library as what is left of them in 32 bits."""
+    x = torch.empty(shape, dtype=BF, device="meta")  # a shape without memory
+    with pytest.raises(ValueError, match="2\\^31"):
+        rs._rows(x, "x", x.get_device())
+
+
+def test_sizes_within_an_int_pass():
+    x = torch.empty((1 << 31) - 1, 0, dtype=BF)
+    assert rs._rows(x, "x", x.get_device())[2] == (1 << 31) - 1
+    assert rs._rows(torch.empty(0, (1 << 31) - 1, dtype=BF), "x", x.get_device())[1] == (1 << 31) - 1
+
+
+def test_scale_bytes_of_sizes_past_an_int():
+    assert rs.rs_fp8_scale_bytes(4, 64) == 512
+    for rows, K in (((1 << 32) + 4, 64), (4, (1 << 32) + 64), (-(1 << 32) + 4, 64)):
+        assert rs.rs_fp8_scale_bytes(rows, K) == 0
+
+
+def test_operand_with_a_negative_width():
+    q = torch.empty(4, 64, dtype=torch.float8_e4m3fn)
+    t = rs.Fp8(q, torch.empty(512, dtype=torch.uint8), 4, -(1 << 32) + 64)
+    with pytest.raises(ValueError, match="shorter than K"):
+        rs._fp8(t, "w", q.get_device())
