@@ -8,7 +8,6 @@ a missing library is an error.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from typing import NamedTuple, Optional, Tuple
 
@@ -585,16 +584,30 @@ def _float_type(x: torch.Tensor) -> int:
     return _DTYPES[x.dtype]
 
 
-@functools.lru_cache(maxsize=4096)
-def _ws_size(name: str, *sizes: int) -> int:
-    return int(getattr(lib(), name)(*sizes))
+_ws_sizes = {}
+
+
+def _ws_size(name: str, *sizes: int, dev: Optional[int] = None) -> int:
+    """What the size function `name` says on device `dev`, the current one. Kept, since a call's
+    host time counts, by device: the layer norm's answer goes by the SM count."""
+    key = (dev, name, sizes)
+    n = _ws_sizes.get(key)
+    if n is None:
+        n = int(getattr(lib(), name)(*sizes))
+        # the layer norm's 0 also says that the device could not be asked, which may pass: it is
+        # kept only where sizes that need scratch get an answer
+        if n or name != "rs_ln_backward_ws_bytes" or lib().rs_ln_backward_ws_bytes(1 << 26, 1):
+            if len(_ws_sizes) >= 4096:
+                _ws_sizes.clear()
+            _ws_sizes[key] = n
+    return n
 
 
 def _ws(ws: Optional[torch.Tensor], device: torch.device, dev: int, name: str, *sizes: int):
     """(address, bytes, tensor) of the caller's scratch, or of scratch from torch's allocator
     (the tensor must live until the call is queued). `name` is the size function."""
     if ws is None:
-        n = _ws_size(name, *sizes)
+        n = _ws_size(name, *sizes, dev=dev)
         if n == 0:  # none needed (or sizes that the call will refuse)
             return None, 0, None
         ws = torch.empty(n, dtype=torch.uint8, device=device)

@@ -33,3 +33,46 @@ def test_operand_with_a_negative_width():
     t = rs.Fp8(q, torch.empty(512, dtype=torch.uint8), 4, -(1 << 32) + 64)
     with pytest.raises(ValueError, match="shorter than K"):
         rs._fp8(t, "w", q.get_device())
+
+
+class _Sizes:
+    """A library whose layer norm needs scratch past 1000 rows: by device, none while it cannot
+    ask the device."""
+
+    def __init__(self):
+        self.sms, self.asked = 0, 0
+
+    def rs_ln_backward_ws_bytes(self, M, C):
+        self.asked += 1
+        return self.sms * 100 if M > 1000 else 0
+
+
+@pytest.fixture
+def sizes(monkeypatch):
+    lib = _Sizes()
+    monkeypatch.setattr(rs, "lib", lambda: lib)
+    monkeypatch.setattr(rs, "_ws_sizes", {}, raising=False)
+
+    def ask(dev, M, sms):
+        lib.sms = sms
+        return rs._ws(None, torch.device("cpu"), dev, "rs_ln_backward_ws_bytes", M, 333)[1]
+    return lib, ask
+
+
+def test_scratch_sizes_are_kept_by_device(sizes):
+    """What one device answered is not another's size."""
+    lib, ask = sizes
+    assert [ask(0, 7001, 10), ask(1, 7001, 20), ask(0, 7001, 10)] == [1000, 2000, 1000]
+    assert lib.asked == 2
+
+
+def test_a_failed_size_query_is_not_kept(sizes):
+    lib, ask = sizes
+    assert [ask(0, 7003, 0), ask(0, 7003, 30), ask(0, 7003, 30)] == [0, 3000, 3000]
+
+
+def test_no_scratch_is_kept_too(sizes):
+    lib, ask = sizes
+    assert ask(0, 12, 10) == 0
+    n = lib.asked
+    assert ask(0, 12, 10) == 0 and lib.asked == n
