@@ -634,7 +634,14 @@ int go(Fp8Gemm p, int num_sms, cudaStream_t s, bool pdl) {
   }
   cudaError_t e;
   if constexpr (PAIR) {
-    static const int max_pairs = [&]() {
+    static std::atomic<int> resident[64];  // pairs at once, by device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+      cudaGetLastError();
+      return RS_ERR_CUDA;
+    }
+    int max_pairs = resident[dev & 63].load(std::memory_order_relaxed);
+    if (max_pairs == 0) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(2 * (num_sms / 2));
       cfg.blockDim = dim3(kGThreads);
@@ -646,13 +653,13 @@ int go(Fp8Gemm p, int num_sms, cudaStream_t s, bool pdl) {
       attr[0].val.clusterDim.z = 1;
       cfg.attrs = attr;
       cfg.numAttrs = 1;
-      int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+      if (cudaOccupancyMaxActiveClusters(&max_pairs, kern, &cfg) != cudaSuccess || max_pairs <= 0) {
         cudaGetLastError();
-        n = num_sms / 2;
+        max_pairs = num_sms / 2;
       }
-      return n < num_sms / 2 ? n : num_sms / 2;
-    }();
+      max_pairs = max_pairs < num_sms / 2 ? max_pairs : num_sms / 2;
+      resident[dev & 63].store(max_pairs, std::memory_order_relaxed);
+    }
     const int pairs = p.num_tiles < max_pairs ? p.num_tiles : max_pairs;
     e = launch_cluster(kern, dim3(2 * pairs), dim3(kGThreads), smem, s, pdl, 2, tA, tB, tSA, tSB, tO,
                        p);
