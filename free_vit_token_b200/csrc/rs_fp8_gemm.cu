@@ -80,6 +80,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
   constexpr int kCols = BN / 4;                     // columns of one epilogue warp
   static_assert(STAGES >= 3, "pipeline depth");
   static_assert(kCols == 32 || kCols == 64, "epilogue columns");
+  static_assert(BN % kQBlock == 0, "a tile's columns start with a scale tile of B");
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -230,12 +231,9 @@ __global__ void __launch_bounds__(kGThreads, 1)
       const uint64_t bd0 = sw128_kmajor_desc(smem_u32(sB));
       const uint64_t sd0 = scale_tile_desc(smem_u32(sS));
       for (int tile = unit0; tile < p.num_tiles; tile += units) {
-        const int n0 = (tile % p.n_blocks) * BN;
         if (!warp_wait(&tempty[acc], acc_phase ^ 1u, wc, true, PAIR)) break;
         tc_fence_after_sync();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
-        // B's columns start inside a scale tile when BN is no multiple of 128: 32 rows a column
-        const uint32_t bcol = 4u + static_cast<uint32_t>((n0 & 127) >> 5);
         bool ok = true;
         for (int kb = 0; kb < KB; ++kb) {
           if (!warp_wait(&full[stage], phase, wc)) { ok = false; break; }
@@ -263,9 +261,9 @@ __global__ void __launch_bounds__(kGThreads, 1)
             for (int k = 0; k < kGK / 32; ++k) {
               if (k == 0 || k < steps) {
                 if constexpr (PAIR)
-                  umma_mx_pair(d_tmem, ad + 2u * k, bd + 2u * k, id, ts, ts + bcol, (kb | k) != 0 ? 1u : 0u);
+                  umma_mx_pair(d_tmem, ad + 2u * k, bd + 2u * k, id, ts, ts + 4u, (kb | k) != 0 ? 1u : 0u);
                 else
-                  umma_mx(d_tmem, ad + 2u * k, bd + 2u * k, id, ts, ts + bcol, (kb | k) != 0 ? 1u : 0u);
+                  umma_mx(d_tmem, ad + 2u * k, bd + 2u * k, id, ts, ts + 4u, (kb | k) != 0 ? 1u : 0u);
               }
             }
             if constexpr (PAIR)
