@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kFThreads)
   const WaitCtl wc{abort_flag, p.err, p.timeout_ns};
 
   if (warp == 0 && elect_one()) {
-    for (int i = 0; i < nb; ++i) {
+    for (int i = p.debug_skip && blockIdx.x == 0 ? 1 : 0; i < nb; ++i) {
       const int kb = kb0 + i;
       const bool scales = i == 0 || (kb & 3) == 0;
       mbar_arrive_expect_tx(&full[i], kFABytes + (scales ? kScaleTile : 0));

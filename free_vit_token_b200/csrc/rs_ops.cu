@@ -337,9 +337,10 @@ uint64_t rs_fp8_linear_ws_bytes(int M, int K) {
   return q_space(M, K).bytes;
 }
 
-int rs_fp8_linear(const void* x, int64_t ldx, int M, int K, int N, const void* wq, int64_t ldw,
-                  const void* scales_w, const void* bias, int gelu, const void* resid, int64_t ldr,
-                  void* out, int64_t ldo, void* ws, uint64_t ws_bytes, void* stream) {
+static int fp8_linear(const void* x, int64_t ldx, int M, int K, int N, const void* wq, int64_t ldw,
+                      const void* scales_w, const void* bias, int gelu, const void* resid,
+                      int64_t ldr, void* out, int64_t ldo, void* ws, uint64_t ws_bytes,
+                      cudaStream_t s, bool debug_skip, unsigned long long timeout_ns) {
   RS_TRY(check_gemm_dims(M, N, K));
   RS_TRY(check_epilogue(bias, gelu, resid, ldr, N, 2));
   if (ldx < K || ldo < N) return RS_ERR_SHAPE;
@@ -347,7 +348,6 @@ int rs_fp8_linear(const void* x, int64_t ldx, int M, int K, int N, const void* w
   if (!x || !out) return RS_ERR_NULL;
   if (!aligned(x, 2) || !aligned(out, 2)) return RS_ERR_ALIGN;
   RS_TRY(check_q(wq, ldw, scales_w, K));
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (rs::fp8_few_rows(M, N, K)) {
     rs::Fp8Few f{};
     f.x = static_cast<const __nv_bfloat16*>(x);
@@ -365,7 +365,8 @@ int rs_fp8_linear(const void* x, int64_t ldx, int M, int K, int N, const void* w
     f.ldr = ldr;
     f.out = static_cast<__nv_bfloat16*>(out);
     f.ldo = ldo;
-    f.timeout_ns = rs::kDefaultTimeoutNs;
+    f.timeout_ns = timeout_ns;
+    f.debug_skip = debug_skip;
     int sms = 0;
     RS_TRY(rs::device_flag(&sms, &f.err));
     return rs::launch_fp8_few(f, sms, s);
@@ -399,6 +400,24 @@ int rs_fp8_linear(const void* x, int64_t ldx, int M, int K, int N, const void* w
   p.ldo = ldo;
   RS_CUDA(rs::launch_quantize(qp, RS_BF16, aligned(x, 16) && ldx % 8 == 0 && K % 8 == 0, s));
   return gemm(p, RS_BF16, s, true);
+}
+
+int rs_fp8_linear(const void* x, int64_t ldx, int M, int K, int N, const void* wq, int64_t ldw,
+                  const void* scales_w, const void* bias, int gelu, const void* resid, int64_t ldr,
+                  void* out, int64_t ldo, void* ws, uint64_t ws_bytes, void* stream) {
+  return fp8_linear(x, ldx, M, K, N, wq, ldw, scales_w, bias, gelu, resid, ldr, out, ldo, ws,
+                    ws_bytes, static_cast<cudaStream_t>(stream), false, rs::kDefaultTimeoutNs);
+}
+
+int rs_debug_fp8_linear_skip_load(const void* x, int64_t ldx, int M, int K, int N, const void* wq,
+                                  int64_t ldw, const void* scales_w, void* out, int64_t ldo,
+                                  int timeout_us, void* stream) {
+  if (M < 1 || !dim_ok(K) || !dim_ok(N) || !rs::fp8_few_rows(M, N, K) || timeout_us < 1 ||
+      timeout_us > 10000000)
+    return RS_ERR_SHAPE;
+  return fp8_linear(x, ldx, M, K, N, wq, ldw, scales_w, nullptr, 0, nullptr, 0, out, ldo, nullptr, 0,
+                    static_cast<cudaStream_t>(stream), true,
+                    static_cast<unsigned long long>(timeout_us) * 1000ull);
 }
 
 uint64_t rs_fp8_linear_backward_ws_bytes(int M, int N) {

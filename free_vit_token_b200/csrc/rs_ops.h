@@ -169,6 +169,7 @@ struct Fp8Few {
   int64_t ldo;
   int* err;
   unsigned long long timeout_ns;
+  bool debug_skip;            // test hook: CTA 0 leaves its first weight tile unloaded
   int split, blocks;          // set by the launcher: CTAs per reduction, K blocks of each
 };
 bool fp8_few_rows(int M, int N, int K);  // does rs_fp8_linear take this path?

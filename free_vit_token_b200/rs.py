@@ -73,6 +73,7 @@ SIGNATURES = {
                          _vp]),
     "rs_debug_fp8_skip_load": (_i, [_vp, _l, _vp, _vp, _l, _vp, _i, _i, _i, _vp, _l, _i, _vp, _i, _i,
                                     _vp]),
+    "rs_debug_fp8_linear_skip_load": (_i, [_vp, _l, _i, _i, _i, _vp, _l, _vp, _vp, _l, _i, _vp]),
     "rs_fp8_linear": (_i, [_vp, _l, _i, _i, _i, _vp, _l, _vp, _vp, _i, _vp, _l, _vp, _l, _vp, _u,
                            _vp]),
     "rs_fp8_linear_ws_bytes": (_u, [_i, _i]),
@@ -943,3 +944,15 @@ def rs_debug_fp8_skip_load(a: Fp8, b: Fp8, out, skip_kblock: int, timeout_us: in
     _check(lib().rs_debug_fp8_skip_load(pa, lda, sa, pb, ldb, sb, M, N, K, po, ldo, dt, so,
                                         int(skip_kblock), int(timeout_us), _stream(stream)),
            "rs_debug_fp8_skip_load")
+
+
+def rs_debug_fp8_linear_skip_load(x: torch.Tensor, w: Fp8, out: torch.Tensor, timeout_us: int,
+                                  stream=None) -> None:
+    """Test hook: rs_fp8_linear on a few rows with one weight tile withheld (see include/rs.h)."""
+    dev = _device(x, "x")
+    px, ldx, M = _rows(x, "x", dev, torch.bfloat16, w.K)
+    pw, ldw, sw = _fp8(w, "w", dev)
+    po, ldo, _ = _rows(out, "out", dev, torch.bfloat16, w.rows, M)
+    _check(lib().rs_debug_fp8_linear_skip_load(px, ldx, M, w.K, w.rows, pw, ldw, sw, po, ldo,
+                                               int(timeout_us), _stream(stream)),
+           "rs_debug_fp8_linear_skip_load")

@@ -485,6 +485,13 @@ int rs_fp8_linear(const void* x, int64_t ldx, int M, int K, int N, const void* w
                   void* out, int64_t ldo, void* ws, uint64_t ws_bytes, void* stream);
 uint64_t rs_fp8_linear_ws_bytes(int M, int K);
 
+/* Test hook of the one-launch form's failure path: rs_fp8_linear (without bias, activation or
+ * residual) on a few rows (others are refused) in which CTA 0 leaves its first weight tile
+ * unloaded, with the consequences that rs_debug_fp8_skip_load lists. */
+int rs_debug_fp8_linear_skip_load(const void* x, int64_t ldx, int M, int K, int N, const void* wq,
+                                  int64_t ldw, const void* scales_w, void* out, int64_t ldo,
+                                  int timeout_us, void* stream);
+
 /* Gradients of out = x W^T + bias for the output gradient dy [M, N] bf16, both products in 8
  * bits with blocks along what they reduce:
  *   dx [M, K] bf16 = dy W      (dy in blocks along N, and W^T: wt [K, ldwt], scales_wt, the

@@ -43,3 +43,18 @@ def test_beside_cta_pairs_of_another_stream():
     assert all(torch.equal(y, want) for y in big)
     assert all(torch.equal(y, z) for y, z in small)
     assert rs.rs_get_last_device_error() == 0
+
+
+# a cluster of several CTAs, one CTA a reduction, up to 32 rows
+@pytest.mark.parametrize("M,N,K", [(8, 1000, 2048), (16, 300, 128), (20, 4096, 640)])
+def test_a_withheld_weight_tile_times_out_and_the_next_call_is_right(M, N, K):
+    rs = _rs()
+    x, w = draw(M, K, BF, 1), rs.rs_fp8_quantize(draw(N, K, BF, 2, 0.0, 0.05))[0]
+    want = rs.rs_fp8_linear(x, w)
+    out = want.clone()
+    assert rs.rs_get_last_device_error() == 0
+    rs.rs_debug_fp8_linear_skip_load(x, w, out, 2000)
+    assert rs.rs_get_last_device_error() == rs.rs.RS_ERR_DEVICE_TIMEOUT
+    assert rs.rs_get_last_device_error() == 0
+    assert torch.equal(rs.rs_fp8_linear(x, w), want)
+    assert rs.rs_get_last_device_error() == 0

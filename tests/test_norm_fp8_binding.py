@@ -76,3 +76,11 @@ def test_no_scratch_is_kept_too(sizes):
     assert ask(0, 12, 10) == 0
     n = lib.asked
     assert ask(0, 12, 10) == 0 and lib.asked == n
+
+
+@pytest.mark.parametrize("M,N,K,us", [(0, 64, 64, 100), (33, 64, 64, 100), (17, 8193, 64, 100), (4, 64, 8193, 100),
+                                      (4, 0, 64, 100), (4, 64, 64, 0), (4, 64, 64, 10000001)])
+def test_withheld_weight_tile_refusals(M, N, K, us):
+    F = 0x100000  # aligned fake device address, never dereferenced on this path
+    assert rs.lib().rs_debug_fp8_linear_skip_load(F, K, M, K, N, F, 16384, F, F, 16384, us, None) \
+        == rs.RS_ERR_SHAPE
