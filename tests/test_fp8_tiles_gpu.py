@@ -124,3 +124,40 @@ def test_mlp_of_several_tiles(M, C, H):
     assert ((got.double() - want).abs() <= tol).all()
     assert (got.double() - want).norm() <= 3e-3 * want.norm()
     assert rs.rs_get_last_device_error() == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(130, 200, 200), (130, 8, 200), (20001, 330, 200), (20001, 1000, 1100)])
+def test_8_bit_output_leaves_the_rest_alone(M, N, K):
+    """Bytes past the row's last 16, rows past the last and scale bytes of neither row nor block."""
+    rs = _rs()
+    a, b = operands(M, N, K, 1)
+    want = rs.rs_fp8_gemm(a, b, out_dtype=E4)
+    ld = -(-N // 16) * 16
+    buf = torch.full((M + 2, ld + 48), 0x55, dtype=torch.uint8, device=dev)
+    sc = torch.full((rs.rs_fp8_scale_bytes(M, N),), 0x55, dtype=torch.uint8, device=dev)
+    out = rs.Fp8(buf[1:M + 1, 16:16 + ld].view(E4), sc, M, N)
+    rs.rs_fp8_gemm(a, b, out=out)
+    assert torch.equal(R.stored(out), R.stored(want))
+    assert (buf[0] == 0x55).all() and (buf[M + 1] == 0x55).all()
+    assert (buf[:, :16] == 0x55).all() and (buf[:, 16 + ld:] == 0x55).all()
+    live = torch.zeros_like(sc, dtype=torch.bool)
+    live[R.scale_index(M, N).flatten().to(dev)] = True
+    assert (sc[~live] == 0x55).all()
+
+
+@pytest.mark.parametrize("M,C", [(130, 200), (3, 1160)])
+def test_8_bit_norm_leaves_the_rest_alone(M, C):
+    rs = _rs()
+    x = draw(M, C, BF, 1)
+    want = rs.rs_ln_quantize(x)
+    buf = torch.full((M + 2, C + 56), 0x55, dtype=torch.uint8, device=dev)
+    buf = buf[:, :(C + 56) // 16 * 16].contiguous()
+    sc = torch.full((rs.rs_fp8_scale_bytes(M, C),), 0x55, dtype=torch.uint8, device=dev)
+    out = rs.Fp8(buf[1:M + 1, 16:].view(E4), sc, M, C)
+    rs.rs_ln_quantize(x, out=out)
+    assert torch.equal(R.stored(out), R.stored(want))
+    assert (buf[0] == 0x55).all() and (buf[M + 1] == 0x55).all()
+    assert (buf[:, :16] == 0x55).all() and (buf[:, 16 + C:] == 0x55).all()
+    live = torch.zeros_like(sc, dtype=torch.bool)
+    live[R.scale_index(M, C).flatten().to(dev)] = True
+    assert (sc[~live] == 0x55).all()
