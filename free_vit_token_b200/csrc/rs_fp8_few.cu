@@ -243,8 +243,9 @@ bool fp8_few_rows(int M, int N, int K) {
 
 int launch_fp8_few(Fp8Few p, int num_sms, cudaStream_t s) {
   const int KB = (p.K + 127) / 128, n_tiles = (p.N + 127) / 128;
-  // CTAs per reduction: enough for 4 blocks each (three such CTAs share an SM, and one loads
-  // while another finishes: 8192 x 2048 8.0 -> 7.0 us), doubled while all of them fit the SMs
+  // CTAs per reduction: enough for 4 blocks each, 85 KB, of which two share an SM and one loads
+  // while the other finishes (8192 x 2048 against 8 blocks each, one CTA on an SM, 8.0 -> 7.0 us),
+  // doubled while all of them fit the SMs
   int split = 1;
   while (split < 8 && split * 4 < KB) split *= 2;
   while (split < 8 && 2 * split <= KB && static_cast<int64_t>(n_tiles) * 2 * split <= num_sms) split *= 2;

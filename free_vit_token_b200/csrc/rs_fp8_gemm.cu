@@ -17,11 +17,12 @@
 //   warp 16    TMA producer, warp 17 TMEM owner and MMA issuer
 // At 8 bits a tile's products take half the time they take in bf16 while its epilogue stays the
 // same: sixteen epilogue warps, not eight, keep up with reductions down to K = 384
-// (50432 x 384 -> 1536 with GELU: 110 us with eight, 82 with sixteen).
+// (50432 x 384 -> 1536 with GELU and its quantiser: 126 us with eight, 106 with sixteen, as both
+// stood then).
 //
 // Measured, back to back: 8192^3 420 us (2.6 PFLOP/s; 300 us with the operand loads left out, and
 // 511 us sustained, where the power cap holds the clock near 1.06 GHz), 25104 x 4096 -> 1024
-// 88 us, 25104 x 1024 -> 4096 103 us, with GELU and 8-bit output 106 us.
+// 88 us, 25104 x 1024 -> 4096 107 us, with GELU and 8-bit output 121 us (on cool caches 116).
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -70,8 +70,8 @@ cudaError_t launch_ln_quantize(const LnForward& p, int dtype, int num_sms, cudaS
 cudaError_t launch_ln_backward(const LnBackward& p, int dtype, bool vec, int num_sms,
                                cudaStream_t s);
 bool ln_backward_few(int M, int C);  // no scratch for these sizes, whatever the type
-// out[c] = sum_p partials[p][c], p ascending by eights, for n columns: the first `split` of
-// them to out0, the others to out1 (either may be null).
+// out[c] = sum_p partials[p][c], in 16 chains (p = i, i + 16, ..) whose sums are added in order,
+// for n columns: the first `split` of them to out0, the others to out1 (either may be null).
 cudaError_t launch_col_reduce(const float* partials, int P, int n, int split, float* out0,
                               float* out1, cudaStream_t stream, bool pdl);
 
